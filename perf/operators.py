@@ -1,11 +1,11 @@
 """Cases of the quantised latent cache: writing it, reading it back, and the
 attention of drafted tokens over it.
 
-A cache row of a token is 656 bytes: 512 e4m3 codes, four float32 scales (one
-for each 128 codes) and 64 bfloat16 values that are kept as they are.  Beside
-it lies the token's indexer key: 128 e4m3 codes and one float32 scale.  Every
-scale is the smallest power of two s with absmax <= 448 s (at least 2^-126;
-1 where all finite values are 0), so code * s is exact in bfloat16.
+A token's latent row of 576 values is kept as 640 bytes: 512 e4m3 codes and 64
+bfloat16 values as they are, and one float32 scale in an array of its own.  Its
+indexer key is kept as 128 e4m3 codes and one float32 scale likewise.  A scale
+is the smallest power of two s >= 2^-32 with absmax <= 448 s over the finite
+values (1 where they are all 0), so code * s is exact in bfloat16.
 
   write   rows [n, 576] and indexer keys [n, 128] go to the physical rows
           slots[n] of the caches (-1: skipped)
@@ -23,7 +23,7 @@ import torch
 
 own = False
 
-ROW, WIDTH, VALUES, KEYS = 656, 576, 512, 128
+ROW, WIDTH, VALUES, KEYS = 640, 576, 512, 128
 TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
 
 
@@ -96,16 +96,17 @@ def values(n, width, g):
 
 
 def filled(rows, g):
-    """A cache in which every row holds a token, and its indexer keys."""
+    """Caches in which every row holds a token: rows, their scales, indexer keys, theirs."""
     cache = torch.empty(rows, ROW, dtype=torch.uint8, device="cuda")
     codes = torch.empty(rows, KEYS, dtype=torch.uint8, device="cuda")
-    scales = torch.empty(rows, device="cuda")
+    row_scales, key_scales = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
     for i in range(0, rows, 1 << 18):
-        x = values(min(rows - i, 1 << 18), WIDTH + KEYS, g)
-        cache[i:i + len(x)] = row_bytes(x[:, :WIDTH])
-        c, s = quantised(x[:, WIDTH:])
-        codes[i:i + len(x)], scales[i:i + len(x)] = c.view(torch.uint8), s
-    return cache, codes, scales
+        at = slice(i, min(rows, i + (1 << 18)))
+        x = values(at.stop - i, WIDTH + KEYS, g)
+        cache[at], row_scales[at] = row_bytes(x[:, :WIDTH])
+        c, key_scales[at] = quantised(x[:, WIDTH:])
+        codes[at] = c.view(torch.uint8)
+    return cache, row_scales, codes, key_scales
 
 
 def prepare(case, seed):
@@ -123,17 +124,17 @@ def prepare(case, seed):
         x = values(n, WIDTH + KEYS, g).to(dt)
         st["kv"], st["k_idx"] = x[:, :WIDTH], x[:, WIDTH:]
         st["cache"] = torch.zeros(rows, ROW, dtype=torch.uint8, device="cuda")
-        st["codes"] = torch.zeros(rows, KEYS, dtype=torch.uint8, device="cuda")
         st["scales"] = torch.zeros(rows, device="cuda")
+        st["keys"] = torch.zeros(rows, KEYS, dtype=torch.uint8, device="cuda")
+        st["key_scales"] = torch.zeros(rows, device="cuda")
         st["out"] = {}
         if st["latent"]:
             st["out"].update(codes=st["cache"][:, :VALUES].view(torch.float8_e4m3fn),
-                             scales=st["cache"][:, VALUES:VALUES + 16].view(torch.float32),
-                             rest=st["cache"][:, VALUES + 16:].view(torch.bfloat16))
+                             rest=st["cache"][:, VALUES:].view(torch.bfloat16), scales=st["scales"])
         if st["index"]:
-            st["out"].update(key_codes=st["codes"].view(torch.float8_e4m3fn), key_scales=st["scales"])
+            st["out"].update(key_codes=st["keys"].view(torch.float8_e4m3fn), key_scales=st["key_scales"])
     else:
-        st["cache"], st["codes"], st["scales"] = filled(rows, g)
+        st["cache"], st["scales"], st["keys"], st["key_scales"] = filled(rows, g)
         st["out"] = {}
         if st["latent"]:
             st["out"]["kv"] = torch.zeros(n, WIDTH, dtype=dt, device="cuda")
@@ -162,8 +163,8 @@ def prepare_attend(case, seed, g):
           "lens": lens.cuda(), "table": table.cuda(),
           "tree": torch.tensor(masks, dtype=torch.int64, device="cuda"),
           "q": torch.randn(B, L, heads, WIDTH, device="cuda", generator=g).bfloat16(),
-          "cache": filled(total * page, g)[0],
           "out": torch.empty(B, L, heads, VALUES, dtype=torch.bfloat16, device="cuda")}
+    st["cache"], st["scales"] = filled(total * page, g)[:2]
     if k:  # positions 0..t of each node, in ascending order, then -1
         t = st["lens"][:, None, None] - L + torch.arange(L, device="cuda")[None, :, None]
         lot = torch.rand(B, L, T, device="cuda", generator=g)
@@ -177,48 +178,45 @@ def prepare_attend(case, seed, g):
 
 # ---------------------------------------------------------------- the plain forms
 def quantised(x):
-    """e4m3 codes and power-of-two scales of groups of 128 along the last axis."""
+    """e4m3 codes of rows and their power-of-two scales."""
     x = x.float()
-    y = x.unflatten(-1, (-1, 128))
-    top = torch.where(torch.isfinite(y), y.abs(), 0.0).amax(-1, keepdim=True)
+    top = torch.where(torch.isfinite(x), x.abs(), 0.0).amax(-1, keepdim=True)
     part, e = torch.frexp(top)  # top = part * 2^e, part in [1/2, 1); 448 = 7/8 * 2^9
-    e = (e - 9 + (part > 0.875)).clamp(min=-126)
+    e = (e - 9 + (part > 0.875)).clamp(min=-32)
     e = torch.where(top > 0, e, 0).to(torch.int32)
     scale, over = ((e + 127) << 23).view(torch.float32), ((127 - e) << 23).view(torch.float32)
-    codes = (y * over).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
-    return codes.flatten(-2), scale.flatten(-2).squeeze(-1)
+    return (x * over).clamp(-448.0, 448.0).to(torch.float8_e4m3fn), scale.squeeze(-1)
 
 
 def row_bytes(kv):
     codes, scales = quantised(kv[:, :VALUES])
-    return torch.cat([codes.view(torch.uint8), scales.view(torch.uint8),
-                      kv[:, VALUES:].to(torch.bfloat16).contiguous().view(torch.uint8)], -1)
+    rest = kv[:, VALUES:].to(torch.bfloat16).contiguous()
+    return torch.cat([codes.view(torch.uint8), rest.view(torch.uint8)], -1), scales
 
 
-def decoded(rows):
-    """float32 [..., 576] of cache rows [..., 656]."""
-    codes = rows[..., :VALUES].view(torch.float8_e4m3fn).float().unflatten(-1, (4, 128))
-    scales = rows[..., VALUES:VALUES + 16].view(torch.float32).unsqueeze(-1)
-    return torch.cat([(codes * scales).flatten(-2), rows[..., VALUES + 16:].view(torch.bfloat16).float()], -1)
+def decoded(rows, scales):
+    """float32 [..., 576] of cache rows [..., 640]."""
+    codes = rows[..., :VALUES].view(torch.float8_e4m3fn).float()
+    return torch.cat([codes * scales.unsqueeze(-1), rows[..., VALUES:].view(torch.bfloat16).float()], -1)
 
 
 def plain_write(st):
     there = st["slots"] >= 0
     at = st["slots"][there].long()
     if st["latent"]:
-        st["cache"][at] = row_bytes(st["kv"][there])
+        st["cache"][at], st["scales"][at] = row_bytes(st["kv"][there])
     if st["index"]:
-        codes, scales = quantised(st["k_idx"][there])
-        st["codes"][at], st["scales"][at] = codes.view(torch.uint8), scales
+        codes, st["key_scales"][at] = quantised(st["k_idx"][there])
+        st["keys"][at] = codes.view(torch.uint8)
     return st["out"]
 
 
 def plain_read(st):
     there, at = (st["slots"] >= 0)[:, None], st["slots"].clamp(min=0).long()
     if st["latent"]:
-        st["out"]["kv"].copy_(torch.where(there, decoded(st["cache"][at]), 0.0))
+        st["out"]["kv"].copy_(torch.where(there, decoded(st["cache"][at], st["scales"][at]), 0.0))
     if st["index"]:
-        x = st["codes"][at].view(torch.float8_e4m3fn).float() * st["scales"][at][:, None]
+        x = st["keys"][at].view(torch.float8_e4m3fn).float() * st["key_scales"][at][:, None]
         st["out"]["k_idx"].copy_(torch.where(there, x, 0.0))
     return st["out"]
 
@@ -232,7 +230,7 @@ def plain_attend(st):
     seen = (at >= 0) & (at < lens) & ((node < 0) | (bit == 1))  # [B, L, keys]
     safe = torch.where((at >= 0) & (at < lens), at, 0)
     row = torch.gather(st["table"].long(), 1, (safe // page).flatten(1)).view(safe.shape) * page + safe % page
-    kv = decoded(st["cache"][row])  # [B, 1 or L, keys, 576]
+    kv = decoded(st["cache"][row], st["scales"][row])  # [B, 1 or L, keys, 576]
     if st["idx"] is None:
         s = torch.matmul(q.flatten(1, 2), kv[:, 0].transpose(1, 2)).view(B, L, heads, -1)
     else:
@@ -264,20 +262,20 @@ def own_run(st):
         st["ws"] = torch.empty(size, dtype=torch.uint8, device="cuda")
         ic.workspace_init(st["ws"])
     if st["op"] == "attend":
-        ic.tree_attn_q8_paged(st["q"], st["cache"], st["idx"], st["pr"], st["scale"], st["out"], st["ws"], tree=st["tree"])
+        ic.tree_attn_q8_paged(st["q"], st["cache"], st["scales"], st["idx"], st["pr"], st["scale"], st["out"], st["ws"], tree=st["tree"])
         return st["out"]
     pick = {}
     if st["op"] == "write":
         if st["latent"]:
-            pick.update(kv=st["kv"], kv_q8=st["cache"])
+            pick.update(kv=st["kv"], kv_q8=st["cache"], kv_scale=st["scales"])
         if st["index"]:
-            pick.update(k_idx=st["k_idx"], k_codes=st["codes"], k_scale=st["scales"])
+            pick.update(k_idx=st["k_idx"], k_codes=st["keys"], k_scale=st["key_scales"])
         ic.cache_write_q8(st["slots"], st["ws"], **pick)
     else:
         if st["latent"]:
-            pick.update(kv=st["out"]["kv"], kv_q8=st["cache"])
+            pick.update(kv=st["out"]["kv"], kv_q8=st["cache"], kv_scale=st["scales"])
         if st["index"]:
-            pick.update(k_idx=st["out"]["k_idx"], k_codes=st["codes"], k_scale=st["scales"])
+            pick.update(k_idx=st["out"]["k_idx"], k_codes=st["keys"], k_scale=st["key_scales"])
         ic.cache_read_q8(st["slots"], st["ws"], **pick)
     return st["out"]
 
@@ -288,7 +286,7 @@ def work(case):
         n = case["n"] - (case["n"] // case["pad"] if case["pad"] else 0)
         size = {"bf16": 2, "f32": 4}[case["dtype"]]
         latent, index = case["what"] != "index", case["what"] != "latent"
-        there = (WIDTH * size + ROW if latent else 0) + (KEYS * size + KEYS + 4 if index else 0)
+        there = (WIDTH * size + ROW + 4 if latent else 0) + (KEYS * size + KEYS + 4 if index else 0)
         padded = (WIDTH * size if latent else 0) + (KEYS * size if index else 0) if case["op"] == "read" else 0
         return {"bytes": n * there + (case["n"] - n) * padded + 4 * case["n"], "flops": 0}
     L, k, heads = case["nodes"], case["k"], case["heads"]
@@ -302,7 +300,7 @@ def work(case):
             pairs += L * context + L * (L + 1) / 2
             rows += T
     queries = case["B"] * L
-    return {"bytes": rows * ROW + queries * (heads * (WIDTH + VALUES) * 2 + 4 * k + 8),
+    return {"bytes": rows * (ROW + 4) + queries * (heads * (WIDTH + VALUES) * 2 + 4 * k + 8),
             "flops": 2.0 * pairs * heads * (WIDTH + VALUES)}
 
 
@@ -319,19 +317,18 @@ def grid(y):
     return torch.clamp(torch.round(y / step) * step, -448.0, 448.0)
 
 
-def group_scale(y):
+def row_scale(y):
     top = y.abs().amax(-1, keepdim=True)
     e = torch.ceil(torch.log2(torch.where(top > 0, top, 448.0) / 448.0))
     e = torch.where(top > 448.0 * two_to(e), e + 1, e)  # what log2 may round at a border
     e = torch.where(top <= 448.0 * two_to(e - 1), e - 1, e)
-    return torch.where(top > 0, two_to(e.clamp(min=-126.0)), 1.0)
+    return torch.where(top > 0, two_to(e.clamp(min=-32.0)), 1.0)
 
 
-def numbers(cache):
+def numbers(cache, scales):
     """float64 [R, 576] of cache rows."""
-    parts = [cache[:, 128 * i:128 * i + 128].view(torch.float8_e4m3fn).double()
-             * cache[:, VALUES + 4 * i:VALUES + 4 * i + 4].view(torch.float32).double() for i in range(4)]
-    return torch.cat(parts + [cache[:, VALUES + 16:].view(torch.bfloat16).double()], 1)
+    return torch.cat([cache[:, :VALUES].view(torch.float8_e4m3fn).double() * scales[:, None].double(),
+                      cache[:, VALUES:].view(torch.bfloat16).double()], 1)
 
 
 def exact(case, seed):
@@ -344,28 +341,25 @@ def exact(case, seed):
         out = {}
         if st["latent"]:
             out["kv"] = torch.zeros(len(slots), WIDTH, dtype=torch.float64, device="cuda")
-            out["kv"][keep] = numbers(st["cache"][slots[keep]])
+            out["kv"][keep] = numbers(st["cache"][slots[keep]], st["scales"][slots[keep]])
         if st["index"]:
             out["k_idx"] = torch.zeros(len(slots), KEYS, dtype=torch.float64, device="cuda")
-            out["k_idx"][keep] = st["codes"][slots[keep]].view(torch.float8_e4m3fn).double() * st["scales"][slots[keep], None].double()
+            out["k_idx"][keep] = st["keys"][slots[keep]].view(torch.float8_e4m3fn).double() * st["key_scales"][slots[keep], None].double()
         return out
     rows, out = case["rows"], {}
     zeros = lambda w: torch.zeros(rows, w, dtype=torch.float64, device="cuda")  # noqa: E731
     if st["latent"]:
-        out.update(codes=zeros(VALUES), scales=zeros(4), rest=zeros(64))
+        out.update(codes=zeros(VALUES), rest=zeros(64), scales=zeros(1)[:, 0])
         x = st["kv"][keep].double()
-        for i in range(4):
-            y = x[:, 128 * i:128 * i + 128]
-            s = group_scale(y)
-            out["codes"][slots[keep], 128 * i:128 * i + 128] = grid(y / s)
-            out["scales"][slots[keep], i] = s[:, 0]
+        y = x[:, :VALUES]
+        out["codes"][slots[keep]] = grid(y / row_scale(y))
+        out["scales"][slots[keep]] = row_scale(y)[:, 0]
         out["rest"][slots[keep]] = x[:, VALUES:]
     if st["index"]:
         out.update(key_codes=zeros(KEYS), key_scales=zeros(1)[:, 0])
         y = st["k_idx"][keep].double()
-        s = group_scale(y)
-        out["key_codes"][slots[keep]] = grid(y / s)
-        out["key_scales"][slots[keep]] = s[:, 0]
+        out["key_codes"][slots[keep]] = grid(y / row_scale(y))
+        out["key_scales"][slots[keep]] = row_scale(y)[:, 0]
     return out
 
 
@@ -376,7 +370,7 @@ def exact_attend(st):
         T = int(st["lens"][b])
         pos = torch.arange(T, device="cuda")
         row = st["table"][b].long()[pos // st["page"]] * st["page"] + pos % st["page"]
-        dense = numbers(st["cache"][row]) if st["idx"] is None else None
+        dense = numbers(st["cache"][row], st["scales"][row]) if st["idx"] is None else None
         for i in range(L):
             mask = int(st["tree"][b, i])
             seen = torch.tensor([True] * (T - L) + [bool(mask >> a & 1) for a in range(L)], device="cuda")
@@ -384,7 +378,7 @@ def exact_attend(st):
                 mine = st["idx"][b, i].long()
                 mine = mine[(mine >= 0) & (mine < T)]
                 mine = mine[seen[mine]]
-                kv = numbers(st["cache"][row[mine]])
+                kv = numbers(st["cache"][row[mine]], st["scales"][row[mine]])
             else:
                 kv = dense[seen]
             if len(kv):

@@ -1,11 +1,12 @@
 """Cases of the quantised latent cache: writing it, reading it back, and the
 attention of drafted tokens over it.
 
-A token's latent row of 576 values is kept as 640 bytes: 512 e4m3 codes and 64
-bfloat16 values as they are, and one float32 scale in an array of its own.  Its
-indexer key is kept as 128 e4m3 codes and one float32 scale likewise.  A scale
-is the smallest power of two s >= 2^-32 with absmax <= 448 s over the finite
-values (1 where they are all 0), so code * s is exact in bfloat16.
+A token's latent row of 576 values is kept as 640 bytes and one float32 scale s
+in an array of its own: 512 e4m3 codes and 64 bfloat16 values, all of them
+divided by s.  Its indexer key is kept as 128 e4m3 codes and one float32 scale
+likewise.  A scale is the smallest power of two s >= 2^-32 with absmax <= 448 s
+over the coded columns' finite values (1 where they are all 0): dividing by it
+and multiplying with it are exact.
 
   write   rows [n, 576] and indexer keys [n, 128] go to the physical rows
           slots[n] of the caches (-1: skipped)
@@ -190,14 +191,14 @@ def quantised(x):
 
 def row_bytes(kv):
     codes, scales = quantised(kv[:, :VALUES])
-    rest = kv[:, VALUES:].to(torch.bfloat16).contiguous()
+    rest = (kv[:, VALUES:].float() / scales[:, None]).to(torch.bfloat16)
     return torch.cat([codes.view(torch.uint8), rest.view(torch.uint8)], -1), scales
 
 
 def decoded(rows, scales):
     """float32 [..., 576] of cache rows [..., 640]."""
     codes = rows[..., :VALUES].view(torch.float8_e4m3fn).float()
-    return torch.cat([codes * scales.unsqueeze(-1), rows[..., VALUES:].view(torch.bfloat16).float()], -1)
+    return torch.cat([codes, rows[..., VALUES:].view(torch.bfloat16).float()], -1) * scales.unsqueeze(-1)
 
 
 def plain_write(st):
@@ -327,8 +328,8 @@ def row_scale(y):
 
 def numbers(cache, scales):
     """float64 [R, 576] of cache rows."""
-    return torch.cat([cache[:, :VALUES].view(torch.float8_e4m3fn).double() * scales[:, None].double(),
-                      cache[:, VALUES:].view(torch.bfloat16).double()], 1)
+    return torch.cat([cache[:, :VALUES].view(torch.float8_e4m3fn).double(),
+                      cache[:, VALUES:].view(torch.bfloat16).double()], 1) * scales[:, None].double()
 
 
 def exact(case, seed):
@@ -354,7 +355,7 @@ def exact(case, seed):
         y = x[:, :VALUES]
         out["codes"][slots[keep]] = grid(y / row_scale(y))
         out["scales"][slots[keep]] = row_scale(y)[:, 0]
-        out["rest"][slots[keep]] = x[:, VALUES:]
+        out["rest"][slots[keep]] = x[:, VALUES:] / row_scale(y)
     if st["index"]:
         out.update(key_codes=zeros(KEYS), key_scales=zeros(1)[:, 0])
         y = st["k_idx"][keep].double()

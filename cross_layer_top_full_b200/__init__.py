@@ -7,7 +7,9 @@ missing this package raises on first use; there is no CPU fallback.
 Entry points mirror ``include/indexcache.h``:
 ``indexer_scores``, ``topk``, ``sparse_attn``, ``layer_stack_forward``,
 their ``*_workspace_size`` queries, ``workspace_init``, ``read_status``,
-``kernel_launches`` and ``status_string``.
+``kernel_launches`` and ``status_string``; the paged calls (``paged_rows``,
+``*_paged``, ``topk_varlen``); and the quantised cache (``cache_write_q8``,
+``cache_read_q8``, ``tree_attn_q8_paged``).
 """
 from __future__ import annotations
 
@@ -25,10 +27,12 @@ __all__ = [
     "layer_stack_forward", "indexer_scores_paged", "topk_varlen_workspace_size", "topk_varlen",
     "indexer_topk_paged_workspace_size", "indexer_topk_paged",
     "sparse_attn_paged_workspace_size", "sparse_attn_paged", "paged_workspace_size",
-    "layer_stack_forward_paged",
+    "layer_stack_forward_paged", "Q8_ROW_BYTES", "Q8_MAX_NODES", "cache_write_q8", "cache_read_q8",
+    "tree_attn_q8_workspace_size", "tree_attn_q8_paged",
 ]
 
 F32, BF16, FP8_E4M3 = 0, 1, 2
+Q8_ROW_BYTES, Q8_MAX_NODES = 640, 64
 STATUS_BYTES = 256
 CUDA_ERROR = -5
 _STATUS = {0: "IC_OK", -1: "IC_ERR_INVALID_ARG", -2: "IC_ERR_PATTERN", -3: "IC_ERR_UNSUPPORTED",
@@ -128,6 +132,17 @@ _SIG = {
                                                     ctypes.POINTER(StackShape),
                                                     ctypes.POINTER(PagedRows), _P,
                                                     ctypes.POINTER(_P), _P, ctypes.c_size_t, _P]),
+    "ic_cache_write_q8": (ctypes.c_int, [_P, ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_int,
+                                         ctypes.c_int64, _P, _P, _P, _P, _P, ctypes.c_int64, _P,
+                                         ctypes.c_size_t, _P]),
+    "ic_cache_read_q8": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int64, ctypes.c_int64, _P,
+                                        ctypes.c_int, _P, ctypes.c_int64, _P, ctypes.c_int64, _P,
+                                        ctypes.c_size_t, _P]),
+    "ic_tree_attn_q8_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(PagedRows), ctypes.c_int,
+                                                         ctypes.c_int]),
+    "ic_tree_attn_q8_paged": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, _P,
+                                             ctypes.POINTER(PagedRows), ctypes.c_int,
+                                             ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -411,3 +426,116 @@ def layer_stack_forward_paged(pattern: str, layers: Sequence[Dict], shape: Stack
                                               ctypes.byref(pr), _ptr(idx_buf), outs, _ptr(ws),
                                               _nbytes(ws), _stream(stream)),
            "ic_layer_stack_forward_paged")
+
+
+# --------------------------------------------------------------------------- quantised cache
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _shaped(x, name: str, dtypes, shape, device, strided: bool = False):
+    """Address of a CUDA tensor on `device` (the current device) of one of
+    `dtypes` whose shape matches (None: any size); contiguous, or with
+    `strided` a 2-D tensor whose rows may lie apart."""
+    _need(x.is_cuda and x.device.index == device,
+          "%s: expected a tensor on cuda:%s, the current device, got %s" % (name, device, x.device))
+    _need(x.dtype in dtypes, "%s: unexpected dtype %s" % (name, x.dtype))
+    _need(x.dim() == len(shape) and all(want is None or have == want
+                                        for have, want in zip(x.shape, shape)),
+          "%s: expected shape %s, got %s" % (name, shape, tuple(x.shape)))
+    if strided:
+        _need(x.shape[0] <= 1 or (x.stride(1) == 1 and x.stride(0) >= x.shape[1]),
+              "%s: expected rows of adjacent values, got strides %s" % (name, x.stride()))
+        _need(x.shape[0] != 1 or x.stride(1) == 1,
+              "%s: expected rows of adjacent values, got strides %s" % (name, x.stride()))
+    else:
+        _need(x.is_contiguous(), "%s: expected a contiguous tensor, got strides %s" % (name, x.stride()))
+    return x.data_ptr()
+
+
+def _row_stride(x) -> int:
+    return max(x.stride(0), x.shape[1])      # one row or none: its stride means nothing
+
+
+def _q8_rows(where, slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale, stream):
+    """The checked arguments that writing and reading share."""
+    import torch
+    device = torch.cuda.current_device()
+    latent, index = kv is not None, k_idx is not None
+    _need(latent or index, "%s: give kv, k_idx or both" % where)
+    _need(latent == (kv_q8 is not None) == (kv_scale is not None) if latent else
+          kv_q8 is None and kv_scale is None, "%s: kv, kv_q8 and kv_scale go together" % where)
+    _need(index == (k_codes is not None) == (k_scale is not None) if index else
+          k_codes is None and k_scale is None, "%s: k_idx, k_codes and k_scale go together" % where)
+    rows = kv if latent else k_idx
+    n, num_rows = rows.shape[0], (kv_q8 if latent else k_codes).shape[0]
+    dtypes = (rows.dtype,) if rows.dtype in (torch.bfloat16, torch.float32) else ()
+    u8 = (torch.uint8, torch.float8_e4m3fn)
+    a = dict(kv=None, kvs=576, kq=None, ks=None, ki=None, kis=128, kc=None, ksc=None)
+    if latent:
+        a["kv"] = _shaped(kv, "kv", dtypes, (n, 576), device, strided=True)
+        a["kvs"] = _row_stride(kv)
+        a["kq"] = _shaped(kv_q8, "kv_q8", (torch.uint8,), (num_rows, Q8_ROW_BYTES), device)
+        a["ks"] = _shaped(kv_scale, "kv_scale", (torch.float32,), (num_rows,), device)
+    if index:
+        a["ki"] = _shaped(k_idx, "k_idx", dtypes, (n, 128), device, strided=True)
+        a["kis"] = _row_stride(k_idx)
+        a["kc"] = _shaped(k_codes, "k_codes", u8, (num_rows, 128), device)
+        a["ksc"] = _shaped(k_scale, "k_scale", (torch.float32,), (num_rows,), device)
+    a["slots"] = None if slots is None else _shaped(slots, "slots", (torch.int32,), (n,), device)
+    a.update(n=n, num_rows=num_rows, dt=F32 if rows.dtype == torch.float32 else BF16,
+             ws=_shaped(ws, "ws", (torch.uint8,), (None,), device), ws_bytes=ws.shape[0],
+             stream=_stream(stream))
+    return a
+
+
+def cache_write_q8(slots, ws, *, kv=None, kv_q8=None, kv_scale=None, k_idx=None, k_codes=None,
+                   k_scale=None, stream=None) -> None:
+    """Quantise the latent rows kv [n, 576] and/or the indexer keys k_idx
+    [n, 128] (bfloat16 or float32; rows may lie apart) into rows slots[n] of
+    the caches kv_q8 [num_rows, 640] uint8 with kv_scale [num_rows], k_codes
+    [num_rows, 128] with k_scale [num_rows].  -1 skips a row; slots None: row
+    n is cache row n.  No two rows may name the same slot."""
+    a = _q8_rows("cache_write_q8", slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale, stream)
+    _check(lib().ic_cache_write_q8(a["kv"], a["kvs"], a["ki"], a["kis"], a["dt"], a["n"], a["slots"],
+                                   a["kq"], a["ks"], a["kc"], a["ksc"], a["num_rows"], a["ws"],
+                                   a["ws_bytes"], a["stream"]), "ic_cache_write_q8")
+
+
+def cache_read_q8(slots, ws, *, kv=None, kv_q8=None, kv_scale=None, k_idx=None, k_codes=None,
+                  k_scale=None, stream=None) -> None:
+    """The reverse of cache_write_q8: rows slots[n] of the caches into kv
+    [n, 576] and/or k_idx [n, 128]; -1 gives a row of zeros."""
+    a = _q8_rows("cache_read_q8", slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale, stream)
+    _check(lib().ic_cache_read_q8(a["kq"], a["ks"], a["kc"], a["ksc"], a["num_rows"], a["n"],
+                                  a["slots"], a["dt"], a["kv"], a["kvs"], a["ki"], a["kis"], a["ws"],
+                                  a["ws_bytes"], a["stream"]), "ic_cache_read_q8")
+
+
+def tree_attn_q8_workspace_size(pr: PagedRows, k: int, Hq: int) -> int:
+    return int(lib().ic_tree_attn_q8_workspace_size(ctypes.byref(pr), k, Hq))
+
+
+def tree_attn_q8_paged(q, kv_q8, kv_scale, idx, pr: PagedRows, scale: float, out, ws, *, tree=None,
+                       stream=None) -> None:
+    """Attention of q [B, Lq, Hq, 576] bf16 over the quantised paged cache
+    (kv_q8 [rows, 640] uint8, kv_scale [rows]); the last Lq cached positions of
+    a sequence are the nodes of a tree of drafted tokens.  tree [B, Lq] int64:
+    bit a of a row is set when it sees node a (None: a chain).  idx [B, Lq, k]
+    int32 restricts a row to the positions it names (None: every position)."""
+    import torch
+    device = torch.cuda.current_device()
+    B, Lq, rows = pr.B, pr.Lq, pr.num_pages * pr.page_size
+    Hq, k = q.shape[-2] if q.dim() == 4 else 0, 0 if idx is None else idx.shape[-1]
+    _need(idx is None or k > 0, "idx: names no position; None stands for every position")
+    _check(lib().ic_tree_attn_q8_paged(
+        _shaped(q, "q", (torch.bfloat16,), (B, Lq, None, 576), device),
+        _shaped(kv_q8, "kv_q8", (torch.uint8,), (rows, Q8_ROW_BYTES), device),
+        _shaped(kv_scale, "kv_scale", (torch.float32,), (rows,), device),
+        None if idx is None else _shaped(idx, "idx", (torch.int32,), (B, Lq, None), device), k,
+        None if tree is None else _shaped(tree, "tree", (torch.int64,), (B, Lq), device),
+        ctypes.byref(pr), Hq, float(scale),
+        _shaped(out, "out", (torch.bfloat16,), (B, Lq, Hq, 512), device),
+        _shaped(ws, "ws", (torch.uint8,), (None,), device), ws.shape[0], _stream(stream)),
+        "ic_tree_attn_q8_paged")

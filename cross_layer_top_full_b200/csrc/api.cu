@@ -527,4 +527,88 @@ ic_status ic_layer_stack_forward_paged(const char* pattern, int n_layers, const 
     return IC_OK;
 }
 
+// ------------------------------------------------------------------ quantised cache
+namespace {
+
+// One call's rows and caches: at least one of the two pairs of arrays, each
+// whole, with row strides that hold a row.
+bool q8_args_ok(const void* kv, int64_t kv_stride, const void* k_idx, int64_t k_stride, ic_dtype dt,
+                int64_t n, const void* kv_q8, const float* kv_scale, const void* k_codes,
+                const float* k_scale, int64_t num_rows) {
+    if (dt != IC_F32 && dt != IC_BF16) return false;
+    if (n < 0 || n > 0x7fffffffLL || num_rows < 0 || num_rows > 0x7fffffffLL) return false;
+    if (n == 0) return true;
+    if (kv == nullptr && k_idx == nullptr) return false;
+    if ((kv != nullptr) != (kv_q8 != nullptr) || (kv != nullptr) != (kv_scale != nullptr)) return false;
+    if ((k_idx != nullptr) != (k_codes != nullptr) || (k_idx != nullptr) != (k_scale != nullptr))
+        return false;
+    const uintptr_t esize = dt == IC_F32 ? 4 : 2;
+    if (kv != nullptr && (kv_stride < 576 || ((uintptr_t)kv_q8 & 15) ||
+                          ((uintptr_t)kv_scale & 3) || (uintptr_t)kv % esize))
+        return false;
+    if (k_idx != nullptr && (k_stride < 128 || ((uintptr_t)k_codes & 15) ||
+                             ((uintptr_t)k_scale & 3) || (uintptr_t)k_idx % esize))
+        return false;
+    return true;
+}
+
+}  // namespace
+
+ic_status ic_cache_write_q8(const void* kv, int64_t kv_row_stride, const void* k_idx,
+                            int64_t k_row_stride, ic_dtype dt, int64_t n, const int32_t* slots,
+                            void* kv_q8, float* kv_scale, void* k_codes, float* k_scale,
+                            int64_t num_rows, void* ws, size_t ws_bytes, void* stream) {
+    if (!q8_args_ok(kv, kv_row_stride, k_idx, k_row_stride, dt, n, kv_q8, kv_scale, k_codes, k_scale,
+                    num_rows))
+        return IC_ERR_INVALID_ARG;
+    if (slots == nullptr && n > num_rows) return IC_ERR_INVALID_ARG;
+    if (!ws_ok(ws, ws_bytes, IC_STATUS_BYTES)) return IC_ERR_WORKSPACE;
+    if (n == 0) return IC_OK;
+    return launch_cache_write_q8(kv, kv_row_stride, k_idx, k_row_stride, dt, n, slots, kv_q8,
+                                 kv_scale, k_codes, k_scale, num_rows, status_of(ws),
+                                 (cudaStream_t)stream);
+}
+
+ic_status ic_cache_read_q8(const void* kv_q8, const float* kv_scale, const void* k_codes,
+                           const float* k_scale, int64_t num_rows, int64_t n, const int32_t* slots,
+                           ic_dtype dt, void* kv, int64_t kv_row_stride, void* k_idx,
+                           int64_t k_row_stride, void* ws, size_t ws_bytes, void* stream) {
+    if (!q8_args_ok(kv, kv_row_stride, k_idx, k_row_stride, dt, n, kv_q8, kv_scale, k_codes, k_scale,
+                    num_rows))
+        return IC_ERR_INVALID_ARG;
+    if (slots == nullptr && n > num_rows) return IC_ERR_INVALID_ARG;
+    if (!ws_ok(ws, ws_bytes, IC_STATUS_BYTES)) return IC_ERR_WORKSPACE;
+    if (n == 0) return IC_OK;
+    return launch_cache_read_q8(kv_q8, kv_scale, k_codes, k_scale, num_rows, n, slots, dt, kv,
+                                kv_row_stride, k_idx, k_row_stride, status_of(ws), (cudaStream_t)stream);
+}
+
+static bool tree_args_ok(const ic_paged_rows* pr, int k, int Hq) {
+    return paged_ok(pr, true) && pr->Lq <= IC_Q8_MAX_NODES && k >= 0 && k <= 16384 && Hq >= 1 &&
+           Hq <= 128;
+}
+
+size_t ic_tree_attn_q8_workspace_size(const ic_paged_rows* pr, int k, int Hq) {
+    if (pr == nullptr || pr->B < 1 || pr->Lq < 1 || pr->Lq > IC_Q8_MAX_NODES || pr->T_max < 1 ||
+        k < 0 || k > 16384 || Hq < 1 || Hq > 128)
+        return IC_STATUS_BYTES;
+    return IC_STATUS_BYTES + align_up(tree_attn_q8_scratch_bytes(*pr, k, Hq));
+}
+
+ic_status ic_tree_attn_q8_paged(const void* q, const void* kv_q8, const float* kv_scale,
+                                const int32_t* idx, int k, const uint64_t* tree,
+                                const ic_paged_rows* pr, int Hq, float scale, void* out, void* ws,
+                                size_t ws_bytes, void* stream) {
+    if (!tree_args_ok(pr, k, Hq) || (k > 0 && pr->B > 0) != (idx != nullptr && pr->B > 0))
+        return IC_ERR_INVALID_ARG;
+    if (!ws_ok(ws, ws_bytes, ic_tree_attn_q8_workspace_size(pr, k, Hq))) return IC_ERR_WORKSPACE;
+    if (pr->B == 0) return IC_OK;
+    if (!q || !kv_q8 || !kv_scale || !out) return IC_ERR_INVALID_ARG;
+    if (((uintptr_t)q & 15) || ((uintptr_t)kv_q8 & 15) || ((uintptr_t)out & 15) ||
+        ((uintptr_t)tree & 7) || ((uintptr_t)idx & 3) || ((uintptr_t)kv_scale & 3))
+        return IC_ERR_INVALID_ARG;
+    return launch_tree_attn_q8(q, kv_q8, kv_scale, idx, k, tree, *pr, Hq, scale, out, status_of(ws),
+                               scratch_of(ws), (cudaStream_t)stream);
+}
+
 }  // extern "C"

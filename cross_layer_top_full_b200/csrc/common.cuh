@@ -17,7 +17,8 @@
 // Launch kinds counted by ic_kernel_launches.
 enum {
     IC_LK_ALL = 0, IC_LK_INDEXER = 1, IC_LK_TOPK = 2, IC_LK_ATTN = 3, IC_LK_COMBINE = 4,
-    IC_LK_INDEXER_TC = 5, IC_LK_ATTN_TC = 6, IC_LK_SELECT = 7, IC_LK_KINDS = 8
+    IC_LK_INDEXER_TC = 5, IC_LK_ATTN_TC = 6, IC_LK_SELECT = 7, IC_LK_CACHE = 8, IC_LK_TREE = 9,
+    IC_LK_KINDS = 10
 };
 
 namespace ic {
@@ -169,5 +170,19 @@ ic_status launch_indexer_tc_paged(const void* q_idx, const float* q_scale, const
 ic_status launch_attn_tc_paged(const void* q, const void* kv_pages, const int32_t* idx, int k,
                                const ic_paged_rows& pr, float scale, void* out, uint32_t* status,
                                void* scratch, size_t scratch_bytes, cudaStream_t s);
+
+// Quantised cache (row format and rules: include/indexcache.h).
+ic_status launch_cache_write_q8(const void* kv, int64_t kv_stride, const void* k_idx,
+                                int64_t k_stride, ic_dtype dt, int64_t n, const int32_t* slots,
+                                void* kv_q8, float* kv_scale, void* k_codes, float* k_scale,
+                                int64_t num_rows, uint32_t* status, cudaStream_t s);
+ic_status launch_cache_read_q8(const void* kv_q8, const float* kv_scale, const void* k_codes,
+                               const float* k_scale, int64_t num_rows, int64_t n, const int32_t* slots, ic_dtype dt,
+                               void* kv, int64_t kv_stride, void* k_idx, int64_t k_stride,
+                               uint32_t* status, cudaStream_t s);
+size_t tree_attn_q8_scratch_bytes(const ic_paged_rows& pr, int k, int Hq);
+ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_scale,
+                              const int32_t* idx, int k, const uint64_t* tree, const ic_paged_rows& pr, int Hq, float scale,
+                              void* out, uint32_t* status, void* scratch, cudaStream_t s);
 
 }  // namespace ic

@@ -118,8 +118,9 @@ ic_status ic_selftest_wait_timeout(void* ws, size_t ws_bytes, void* stream);
  * 0 = all, 1 = indexer, 2 = top-k, 3 = attention, 4 = split-k combine,
  * 5 = indexer launches that took the tensor-core path, 6 = attention
  * launches that took the tensor-core path, 7 = fused decode key selections
- * (each also counted once under 1 and once under 2).  A host-side diagnostic
- * counter (thread-safe). */
+ * (each also counted once under 1 and once under 2), 8 = quantised cache
+ * writes and reads, 9 = attention over the quantised cache (its split-k
+ * combine counts under 4).  A host-side diagnostic counter (thread-safe). */
 uint64_t ic_kernel_launches(int kind);
 
 /* ------------------------------------------------------------------------ */
@@ -406,6 +407,113 @@ ic_status ic_layer_stack_forward_paged(const char* pattern, int n_layers,
                                        const ic_paged_rows* pr, int32_t* idx_buf,
                                        int32_t* const* idx_out, void* ws, size_t ws_bytes,
                                        void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* The quantised cache: writing it, reading it back, attending over it       */
+/* ------------------------------------------------------------------------ */
+/*
+ * A cache that keeps a token's latent KV row of 576 values in 640 + 4 bytes
+ * instead of the 1152 of IC_BF16, and its indexer key in 128 + 4 (the paged
+ * caches of ic_indexer_scores_paged with IC_FP8_E4M3):
+ *
+ *   kv_q8     640 bytes per row: bytes 0..511 the e4m3 codes of columns
+ *             0..511, bytes 512..639 columns 512..575 divided by the row's
+ *             scale, as bfloat16
+ *   kv_scale  one float32 scale per row
+ *   k_codes   128 e4m3 codes per row;  k_scale  one float32 scale per row
+ *
+ * The scale of a row x is the smallest power of two s >= 2^-32 with max|x| <=
+ * 448 s over the finite values of its coded columns (1 when they are all
+ * zero); a code is x / s rounded to the nearest e4m3 value, ties to the even one, with
+ * magnitudes above 448 (infinities) at 448 and NaN kept as NaN.  A power of
+ * two costs no accuracy in a floating-point code, and it makes the division
+ * and the product with s exact in bfloat16 (inside its range): what is read
+ * back is exactly what the cache stands for.  With every column of a row
+ * under the one scale, a dot product with the row needs it once, at its end.
+ *
+ * `slots` names physical cache rows: row n of a call is cache row slots[n]
+ * (for a paged sequence block_table[s / page_size] * page_size + s %
+ * page_size).  -1 is a padding row.  Any other value outside [0, num_rows)
+ * is treated as -1 and sets the status bit IC_ERR_INDEX_RANGE.  slots may be
+ * NULL: row n is cache row n.  Row offsets are 64-bit: caches may pass 4 GiB.
+ */
+#define IC_Q8_ROW_BYTES 640
+#define IC_Q8_MAX_NODES 64
+
+/* Quantise n tokens into the caches, in one launch.
+ *   kv        [n, 576] of dt (IC_BF16 or IC_F32), consecutive rows
+ *             kv_row_stride elements apart (>= 576); NULL: no latent rows
+ *   k_idx     [n, 128] of dt, consecutive rows k_row_stride elements apart
+ *             (>= 128); NULL: no indexer keys (an S layer has none)
+ *   slots     [n] int32.  Two rows of one call must not name the same slot:
+ *             what that slot then holds is unspecified.
+ *   kv_q8     [num_rows, IC_Q8_ROW_BYTES] bytes, 16-byte aligned (output)
+ *   kv_scale  [num_rows] float32 (output)
+ *   k_codes   [num_rows, 128] e4m3, 16-byte aligned (output)
+ *   k_scale   [num_rows] float32 (output)
+ * Cache rows that no slot names are left as they were.  Columns 512..575 of
+ * IC_F32 rows are rounded to bfloat16 (to an infinity where the quotient with
+ * the scale passes the largest one).  Inputs may have any element
+ * alignment; rows that start on 16-byte boundaries are read as vectors.
+ * Workspace: IC_STATUS_BYTES. */
+ic_status ic_cache_write_q8(const void* kv, int64_t kv_row_stride, const void* k_idx,
+                            int64_t k_row_stride, ic_dtype dt, int64_t n, const int32_t* slots,
+                            void* kv_q8, float* kv_scale, void* k_codes, float* k_scale,
+                            int64_t num_rows, void* ws, size_t ws_bytes, void* stream);
+
+/* The reverse: n rows of the caches as dt (the input of ic_sparse_attn for a
+ * chunk of a prompt, for example).
+ *   kv        [n, 576] of dt (IC_BF16 or IC_F32), consecutive rows
+ *             kv_row_stride elements apart (output); NULL: not read
+ *   k_idx     [n, 128] of dt, likewise (output); NULL: not read
+ *   slots     [n] int32; a slot may be named more than once
+ * A padding row reads as zeros.  Only the 576 (128) columns of a row are
+ * written.  Scales that are not powers of two (indexer keys quantised by
+ * other rules) are multiplied in float32 and the product rounded once to dt.
+ * Workspace: IC_STATUS_BYTES. */
+ic_status ic_cache_read_q8(const void* kv_q8, const float* kv_scale, const void* k_codes,
+                           const float* k_scale, int64_t num_rows, int64_t n,
+                           const int32_t* slots, ic_dtype dt, void* kv, int64_t kv_row_stride,
+                           void* k_idx, int64_t k_row_stride, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* Attention of a tree of drafted tokens (or of one new token) over the
+ * quantised paged cache.  The last Lq = pr->Lq cached positions of sequence b,
+ * C_b .. seq_lens[b] - 1 with C_b = seq_lens[b] - Lq, are the nodes of a
+ * tree; node i is position C_b + i and query row i.  Row (b, i) sees
+ *   - every position before C_b, and
+ *   - node a exactly when bit a of tree[b*Lq + i] is set (a < Lq; a node's
+ *     own bit counts like any other),
+ * restricted to the positions that idx[b, i, :] names, when idx is given:
+ *     p_s = softmax_s(scale * q[b,i,h,:] . KV[s, 0:576]),
+ *     out[b,i,h,:] = sum_s p_s KV[s, 0:512]       over the seen positions s.
+ *
+ *   q         [B, Lq, Hq, 576] bf16, Hq in [1, 128], 16-byte aligned
+ *   kv_q8     [num_pages*page_size, IC_Q8_ROW_BYTES], 16-byte aligned
+ *   kv_scale  [num_pages*page_size] float32, powers of two as the write gives
+ *   idx       [B, Lq, k] int32 logical positions, or -1 (skipped, anywhere in
+ *             the row).  A node that the row does not see is skipped too.  A
+ *             position outside [0, seq_lens[b]) and not -1 is skipped and
+ *             sets the status bit IC_ERR_INDEX_RANGE.  A position named twice
+ *             counts twice.  NULL with k = 0: every position (a context no
+ *             longer than the selection needs no selection).
+ *   k         0 (idx NULL) or [1, 16384]
+ *   tree      [B, Lq] uint64 bit masks, 8-byte aligned; bits >= Lq are
+ *             ignored.  NULL: a chain (row i sees nodes 0..i).
+ *   pr        Lq in [1, IC_Q8_MAX_NODES]; otherwise as the other paged calls
+ *             (a length outside [Lq, T_max] gives the sequence zero rows and
+ *             the status bit).  A block-table entry outside the cache hides
+ *             its positions and sets the status bit.
+ *   out       [B, Lq, Hq, 512] bf16, 16-byte aligned.  A row that sees
+ *             nothing gets zeros.
+ * A NaN or infinity in a cache row that a query row does not see does not
+ * reach that row's output; a NaN in a seen row makes it NaN.
+ * Workspace: ic_tree_attn_q8_workspace_size(pr, k, Hq). */
+size_t ic_tree_attn_q8_workspace_size(const ic_paged_rows* pr, int k, int Hq);
+ic_status ic_tree_attn_q8_paged(const void* q, const void* kv_q8, const float* kv_scale,
+                                const int32_t* idx, int k, const uint64_t* tree,
+                                const ic_paged_rows* pr, int Hq, float scale, void* out,
+                                void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

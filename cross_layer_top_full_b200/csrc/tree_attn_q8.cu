@@ -1,150 +1,929 @@
 // tree_attn_q8.cu -- attention of a tree of drafted tokens over the quantised
-// paged cache (see include/indexcache.h).
+// paged cache (see include/indexcache.h) on the tcgen05 tensor cores.
 //
 // Row (b, i), head h, over the seen positions s (before the tree, or a node of
-// the row's mask; restricted to idx[b,i,:] where it is given):
-//   p = softmax_s(scale * q . KV[s, 0:576]),  out = sum_s p_s KV[s, 0:512].
+// the row's mask; restricted to idx[b,i,:] where it is given), with g_s the
+// cache row's scale and c_s its 576 scaled values:
+//   p = softmax_s(scale * g_s (q . c_s)),  out = sum_s (p_s g_s) c_s[0:512].
 //
-// Simple form: one CTA per (row, 8 heads).  Tiles of 32 positions are decoded
-// to float32 in shared memory; a warp computes the logits of one head and the
-// online softmax, then every thread accumulates two columns of all 8 heads.
+// The cache's codes go into the products as they are; nothing is decoded.
+//   Q K^T: a query value has 8 significant bits, an e4m3 number 4, so with a
+//     power-of-two scale per row q = hi + lo exactly, two e4m3 numbers (lo's
+//     floor is 2^-18 of the row's largest value).  The 64 columns that the
+//     cache keeps as bfloat16 follow in the same accumulator: both operands
+//     carry the same scales there.
+//   P V: the weights w_s = p_s g_s go in as an e4m3 number and an e5m2 number
+//     for the rest: 7 significant bits down to 2^-10 of the row's largest
+//     weight, 3 down to 2^-18, so that many small weights beside a large one
+//     are not lost.  The running maximum is that of log2 w_s, which keeps w
+//     in 8-bit range whatever the scales are; the largest weight stands
+//     between 2^4 and 2^8.  The softmax sum adds w_s / g_s in float32.
+// Two 8-bit products cost what one of bfloat16 does, without the decoding and
+// with 644 bytes of cache traffic per row.
+//
+// A unit is 128 query rows that read the same positions: the heads of one row
+// (idx given), or 128 consecutive (node, head) pairs of a sequence.  All
+// units' blocks of 128 positions are one list, cut into equal runs, one per
+// CTA pair; where a run ends inside a unit, the pair leaves a float32 partial
+// result and a second kernel joins them.
+//
+// A pair works on one unit at a time: each CTA holds 64 of the rows, gathers
+// 64 of the block's 128 keys whole (for Q K^T) and half of the value columns
+// of all 128 (for P V): an M = 128 product of a pair takes its B operand in
+// two halves, split by keys for the one and by columns for the other.
+//   warps 0-7  softmax (thread = row x 32 keys), conversion of Q, epilogue
+//   warp 8     resolves positions to cache rows; TMA (one box per 64
+//              consecutive rows, four-row gathers otherwise; a row that
+//              nobody may see becomes an out-of-range row, which TMA fills
+//              with zeros); scales and masks of the block
+//   warp 9     rank 0: issues the MMAs: S(j+1) before P V(j), so that the
+//              softmax of a block runs under the next block's Q K^T;
+//              rank 1: tells rank 0 when its own tiles have landed
+// Tensor memory: O 256 columns, two S buffers of 64, Q's bfloat16 columns 32,
+// one of Q's eight 8-bit slices 32.  Shared memory: seven slices of Q 56 KB,
+// K 2 x 40 KB, V 2 x 32 KB, P 16 KB.
+//
+// Every wait is bounded (sm100.cuh); sites: 1-4 producer, 5-9 softmax, 10-16
+// MMA issuer, 17-18 relay.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 
 #include "q8.cuh"
+#include "sm100.cuh"
 
 namespace ic {
 namespace {
 
 using namespace q8;
+using namespace sm100;
 
-constexpr int HG = 8, KT = 32, THREADS = 256;
+constexpr int MROWS = 128, HROWS = 64;        // query rows of a unit, of a CTA
+constexpr int NB = 128;                       // positions per block
+constexpr int ATOM = 64 * 128;                // 64 rows of 128 bytes
+constexpr int Q_SMEM = 7;                     // slices of Q in shared memory: hi 0-3, lo 0-2
+constexpr int K_STAGE = 5 * ATOM, V_STAGE = 4 * ATOM;
+constexpr int OFF_Q = 0;
+constexpr int OFF_K = OFF_Q + Q_SMEM * ATOM;
+constexpr int OFF_V = OFF_K + 2 * K_STAGE;
+constexpr int OFF_P = OFF_V + 2 * V_STAGE;
+constexpr int OFF_SC = OFF_P + 2 * ATOM;      // [2][3][128] float: scale, its log2, its inverse
+constexpr int OFF_XM = OFF_SC + 2 * 3 * NB * 4;       // [2][4][64] float: row maxima
+constexpr int OFF_XL = OFF_XM + 2 * 4 * HROWS * 4;    // [4][64] float: row sums
+constexpr int OFF_SQ = OFF_XL + 4 * HROWS * 4;        // [64] float: scales of Q's rows
+constexpr int OFF_MASK = OFF_SQ + HROWS * 4;          // [2][4] uint32: seen positions of a block
+constexpr int OFF_BARS = OFF_MASK + 32;
+constexpr int SOFT_WARPS = 8, W_LOAD = 8, W_MMA = 9;
+constexpr int THREADS = 32 * 10;
+constexpr uint32_t TM_O = 0, TM_S = 256, TM_QR = 384, TM_QL = 416;
+constexpr int TMEM_COLS = 512;
+constexpr int MAX_PAIRS = 74;                 // CTA pairs of 148 SMs
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float TOP = 4.f, SLACK = 4.f;       // log2 of the largest weight when the maximum is
+                                              // set, and how far it may grow before O is rescaled
 
-__global__ void __launch_bounds__(THREADS)
-tree_attn_simple_kernel(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ cache,
-                        const float* __restrict__ kv_scale,
-                        const int32_t* __restrict__ idx, int k, const unsigned long long* __restrict__ tree,
-                        ic_paged_rows pr, int Hq, float scale, __nv_bfloat16* __restrict__ out,
-                        uint32_t* status) {
-    extern __shared__ float sm[];
-    float* qs = sm;                  // [HG][576]
-    float* ks = qs + HG * KVW;       // [KT][577]
-    float* ps = ks + KT * (KVW + 1); // [HG][KT]
-    float* corr = ps + HG * KT;      // [HG]
-    float* linv = corr + HG;         // [HG]
-    __shared__ int seen[KT];
-    const int row = blockIdx.x, h0 = blockIdx.y * HG;
-    const int b = row / pr.Lq, i = row % pr.Lq;
-    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    pdl_trigger();
+struct __align__(8) Bars {
+    uint64_t q_full;                 // rank 0: Q of a unit is in place (both CTAs' warps)
+    uint64_t k_full[2], v_full[2];   // own tiles have landed
+    uint64_t k_peer[2], v_peer[2];   // rank 0: rank 1's tiles have landed
+    uint64_t sc_full[2];             // scales and masks of a block
+    uint64_t s_full[2];              // S of a block is complete: K stage free
+    uint64_t p_full;                 // rank 0: P of a block is in place (both CTAs' warps)
+    uint64_t pv_done[2];             // P V of a block is complete: V stage, P free
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    int start_b, start_u, start_t;
+    int pad;
+    long long left;
+};
+constexpr size_t SMEM_BYTES = 1008 + OFF_BARS + sizeof(Bars);
+static_assert(SMEM_BYTES <= 232448 && OFF_BARS % 8 == 0, "shared memory budget");
+
+struct Args {
+    const __nv_bfloat16* q;
+    const float* kv_scale;
+    const int32_t* idx;
+    const unsigned long long* tree;
+    const int32_t* seq_lens;
+    const int32_t* block_table;
+    __nv_bfloat16* out;
+    float* part_o;      // [2 * pairs][128][512]
+    float2* part_ml;    // [2 * pairs][128]: running maximum, sum
+    uint32_t* status;
+    int k, B, Lq, Hq, T_max, max_pages, page_size, num_pages;
+    int units;          // per sequence
+    int list_blocks;    // blocks of a list (idx given)
+    float scale_log2;
+};
+
+// ------------------------------------------------------------------ the list of blocks
+__device__ __forceinline__ int seq_len(const Args& a, int b) {
+    const int len = __ldg(a.seq_lens + b);
+    return len < a.Lq || len > a.T_max ? 0 : len;
+}
+__device__ __forceinline__ int blocks_of(const Args& a, int b) {
+    return a.idx ? a.list_blocks : max(1, (seq_len(a, b) + NB - 1) / NB);
+}
+
+// All blocks of the call (one warp).
+__device__ __forceinline__ long long total_blocks(const Args& a) {
+    if (a.idx) return (long long)a.B * a.units * a.list_blocks;
+    long long n = 0;
+    for (int b = threadIdx.x & 31; b < a.B; b += 32) n += blocks_of(a, b);
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n * a.units;
+}
+
+// Runs of the pairs: pair p of P takes blocks [p n / P, (p+1) n / P).
+__device__ __forceinline__ int pairs_of(long long n, int max_pairs) { return n < max_pairs ? (int)n : max_pairs; }
+__device__ __forceinline__ long long run_begin(long long n, int P, int p) { return n * p / P; }
+__device__ __forceinline__ int pair_with(long long n, int P, long long t) { return (int)(((t + 1) * P - 1) / n); }
+
+// A walk over a run: unit u of sequence b, from block t on.
+struct Walk {
+    int b, u, t, nt;
+    long long left;
+    __device__ __forceinline__ void start(const Args& a, const Bars& s) {
+        b = s.start_b; u = s.start_u; t = s.start_t; left = s.left;
+        nt = left > 0 ? blocks_of(a, b) : 0;
+    }
+    __device__ __forceinline__ int count() const { return left < nt - t ? (int)left : nt - t; }
+    __device__ __forceinline__ void next(const Args& a) {
+        left -= count();
+        t = 0;
+        if (++u == a.units) {
+            u = 0;
+            ++b;
+            if (left > 0) nt = blocks_of(a, b);
+        }
+    }
+};
+
+// Query rows of a unit: first + m for m in [0, rows).
+struct Rows {
+    int64_t first;
+    int rows, node0;      // rows (at most 128); (node, head) index of the first in its sequence
+};
+__device__ __forceinline__ Rows unit_rows(const Args& a, int b, int u) {
+    Rows r;
+    if (a.idx) {
+        r.node0 = u * a.Hq;
+        r.rows = a.Hq;
+    } else {
+        r.node0 = u * MROWS;
+        r.rows = min(MROWS, a.Lq * a.Hq - r.node0);
+    }
+    r.first = (int64_t)b * a.Lq * a.Hq + r.node0;
+    return r;
+}
+
+// ------------------------------------------------------------------ small helpers
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 f2_split(uint64_t v) {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return make_float2(a, b);
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two e4m3 numbers and two e5m2 numbers for what they leave of (a, b).
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const float2 h = decode2(hi);
+    lo = __nv_cvt_float2_to_fp8x2(make_float2(a - h.x, b - h.y), __NV_SATFINITE, __NV_E5M2);
+}
+
+// Four scaled query values (two bfloat16 pairs) as e4m3 numbers and e4m3
+// numbers for what they leave.  An infinity becomes a NaN (its row is lost).
+__device__ __forceinline__ float4 scaled4(uint32_t p0, uint32_t p1, float inv) {
+    float4 v = make_float4(__uint_as_float(p0 << 16) * inv, __uint_as_float(p0 & 0xffff0000u) * inv,
+                           __uint_as_float(p1 << 16) * inv, __uint_as_float(p1 & 0xffff0000u) * inv);
+    v.x += v.x - v.x; v.y += v.y - v.y; v.z += v.z - v.z; v.w += v.w - v.w;
+    return v;
+}
+__device__ __forceinline__ uint32_t high4(float4 v) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v.x, v.y), __NV_SATFINITE, __NV_E4M3) |
+           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v.z, v.w), __NV_SATFINITE, __NV_E4M3) << 16;
+}
+__device__ __forceinline__ uint32_t low4(float4 v, uint32_t hi) {
+    const float2 a = decode2(hi), b = decode2(hi >> 16);
+    return high4(make_float4(v.x - a.x, v.y - a.y, v.z - b.x, v.w - b.y));
+}
+
+// Largest finite magnitude of a bfloat16 pair, as float32 bits.
+__device__ __forceinline__ uint32_t pair_max(uint32_t p) {
+    return max(finite_abs_bits(__uint_as_float(p << 16)), finite_abs_bits(__uint_as_float(p & 0xffff0000u)));
+}
+
+// Bits of the 32 positions from s0 on that a row sees by its tree mask.
+__device__ __forceinline__ uint32_t tree_bits(unsigned long long mask, int off) {   // off = s0 - ctx
+    if (off <= -32) return 0xffffffffu;
+    if (off >= 0) return off < 64 ? (uint32_t)(mask >> off) : 0u;
+    return (uint32_t)(mask << -off) | ((1u << -off) - 1u);
+}
+
+// ------------------------------------------------------------------ Q of a unit
+// The 64 rows of this CTA, 256 threads.  Returns this thread's row's scale
+// (row = lane of the quadrant & 63).
+__device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t* smem, uint32_t rank,
+                                           uint32_t tmem, uint32_t lane_base) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* sq = reinterpret_cast<float*>(smem + OFF_SQ);
+    const int64_t first = r.first + rank * HROWS;
+    const int rows = r.rows - (int)rank * HROWS;
+    uint4 v[8][2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = warp * 8 + i;
+        const uint4* p = reinterpret_cast<const uint4*>(a.q + (first + row) * KVW + lane * 16);
+        const bool ok = row < rows;
+        v[i][0] = ok ? __ldg(p) : make_uint4(0u, 0u, 0u, 0u);
+        v[i][1] = ok ? __ldg(p + 1) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = warp * 8 + i;
+        uint32_t m = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            m = max(m, max(max(pair_max(v[i][h].x), pair_max(v[i][h].y)), max(pair_max(v[i][h].z), pair_max(v[i][h].w))));
+        const int e = scale_exponent(__reduce_max_sync(0xffffffffu, m));
+        const float inv = exp2_int(-e);
+        if (lane == 0) sq[row] = exp2_int(e);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 x = scaled4(v[i][h].x, v[i][h].y, inv), y = scaled4(v[i][h].z, v[i][h].w, inv);
+            hi[2 * h] = high4(x);
+            hi[2 * h + 1] = high4(y);
+            lo[2 * h] = low4(x, hi[2 * h]);
+            lo[2 * h + 1] = low4(y, hi[2 * h + 1]);
+        }
+        uint8_t* d = smem + OFF_Q + (lane >> 3) * ATOM + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (lane < 24) *reinterpret_cast<uint4*>(d + 4 * ATOM) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    soft_sync();
+    // tensor memory: the bfloat16 columns (warps 0-3), the last slice of lo (warps 4-7)
+    const int row = (warp & 1) * 32 + lane;
+    const float scale = sq[row], inv = 1.f / scale;
+    const bool ok = row < rows;
+    uint32_t w[32];
+    if (warp < 4) {
+        const uint4* p = reinterpret_cast<const uint4*>(a.q + (first + row) * KVW + DV);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint4 x = ok ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[4 * i + j] = bf16_pair(__uint_as_float(u[j] << 16) * inv, __uint_as_float(u[j] & 0xffff0000u) * inv);
+        }
+        tmem_st32(tmem + lane_base + TM_QR, w);
+    } else {
+        const uint4* p = reinterpret_cast<const uint4*>(a.q + (first + row) * KVW + 384);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint4 x = ok ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
+            const float4 y = scaled4(x.x, x.y, inv), z = scaled4(x.z, x.w, inv);
+            w[2 * i] = low4(y, high4(y));
+            w[2 * i + 1] = low4(z, high4(z));
+        }
+        tmem_st32(tmem + lane_base + TM_QL, w);
+    }
+    tmem_st_wait();
+    return scale;
+}
+
+// ------------------------------------------------------------------ the kernel
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+tree_attn_kernel(const __grid_constant__ CUtensorMap map_rows,    // box: 1 row x 128 bytes
+                 const __grid_constant__ CUtensorMap map_box,     // box: 64 rows x 128 bytes
+                 const __grid_constant__ Args a) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    Bars& s = *reinterpret_cast<Bars*>(smem + OFF_BARS);
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    volatile int* abort = &s.abort;
+    uint32_t* status = a.status;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&s.q_full, 2 * SOFT_WARPS);
+        mbar_init(&s.p_full, 2 * SOFT_WARPS);
+        mbar_init(&s.drain, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.k_full[i], 1);
+            mbar_init(&s.v_full[i], 1);
+            mbar_init(&s.k_peer[i], 1);
+            mbar_init(&s.v_peer[i], 1);
+            mbar_init(&s.sc_full[i], 32);
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.pv_done[i], 1);
+        }
+        s.abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&map_rows);
+        tma_prefetch_desc(&map_box);
+    }
+    if (warp == W_MMA) tmem_alloc_pair<TMEM_COLS>(&s.tmem_base);
     pdl_wait();
-    int len = pr.seq_lens[b];
-    if (len < pr.Lq || len > pr.T_max) {
-        if (t == 0) flag_status(status, IC_DEV_INDEX_RANGE);
-        len = 0;
-    }
-    const int ctx = len - pr.Lq;
-    const unsigned long long own = i >= 63 ? ~0ull : (2ull << i) - 1;
-    const unsigned long long mask = tree ? tree[row] : own;
-    for (int c = t; c < HG * KVW; c += THREADS) {
-        const int h = h0 + c / KVW;
-        qs[c] = h < Hq ? __bfloat162float(q[((int64_t)row * Hq + h) * KVW + c % KVW]) * scale : 0.f;
-    }
-    float m = -INFINITY, l = 0.f, acc[HG][2];
-    for (int h = 0; h < HG; ++h) acc[h][0] = acc[h][1] = 0.f;
-    const int n = len == 0 ? 0 : idx ? k : len;
-    for (int j0 = 0; j0 < n; j0 += KT) {
-        __syncthreads();
-        for (int kk = warp; kk < KT; kk += THREADS / 32) {
-            int s = -1;
-            if (j0 + kk < n) s = idx ? idx[(int64_t)row * k + j0 + kk] : j0 + kk;
-            if (s != -1 && (s < 0 || s >= len)) {
-                if (lane == 0) flag_status(status, IC_DEV_INDEX_RANGE);
-                s = -1;
-            }
-            if (s >= 0 && s >= ctx && !((mask >> (s - ctx)) & 1)) s = -1;
-            int64_t phys = -1;
-            if (s >= 0) {
-                const int page = pr.block_table[(int64_t)b * pr.max_pages + s / pr.page_size];
-                if (page < 0 || page >= pr.num_pages) {
-                    if (lane == 0) flag_status(status, IC_DEV_INDEX_RANGE);
-                } else {
-                    phys = (int64_t)page * pr.page_size + s % pr.page_size;
+    if (warp == W_LOAD) {            // this pair's run
+        const long long n = total_blocks(a);
+        const int P = pairs_of(n, gridDim.x / 2), p = blockIdx.x / 2;
+        long long begin = 0, left = 0;
+        if (p < P) {
+            begin = run_begin(n, P, p);
+            left = run_begin(n, P, p + 1) - begin;
+        }
+        int b = 0;
+        long long off = begin;       // blocks between sequence b's first and the run's first
+        if (a.idx) {
+            const long long per = (long long)a.units * a.list_blocks;
+            b = (int)(begin / per);
+            off = begin % per;
+        } else if (left > 0) {
+            for (int b0 = 0; b0 < a.B; b0 += 32) {
+                const long long c = b0 + lane < a.B ? (long long)blocks_of(a, b0 + lane) * a.units : 0;
+                long long x = c;     // inclusive prefix sum
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
                 }
-            }
-            if (lane == 0) seen[kk] = phys >= 0;
-            const uint8_t* p = cache + phys * ROW;
-            for (int c = lane; c < KVW; c += 32) {
-                float v = 0.f;
-                if (phys >= 0) {
-                    if (c < DV) v = decode2(p[c]).x;
-                    else v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p + OFF_ROPE + 2 * (c - DV)));
-                    v *= kv_scale[phys];
+                const unsigned hit = __ballot_sync(0xffffffffu, off < x);
+                if (hit) {
+                    const int l = __ffs(hit) - 1;
+                    b = b0 + l;
+                    off -= __shfl_sync(0xffffffffu, x - c, l);
+                    break;
                 }
-                ks[kk * (KVW + 1) + c] = v;
+                off -= __shfl_sync(0xffffffffu, x, 31);
             }
         }
-        __syncthreads();
-        {   // warp = head, lane = position
-            float x = 0.f;
-            for (int c = 0; c < KVW; ++c) x = fmaf(qs[warp * KVW + c], ks[lane * (KVW + 1) + c], x);
-            if (!seen[lane]) x = -INFINITY;
-            float mx = x;
-            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-            mx = fmaxf(mx, m);
-            const float a = m == -INFINITY ? 0.f : __expf(m - mx);
-            const float p = !seen[lane] ? 0.f : __expf(x - mx);
-            float sum = p;
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-            l = l * a + sum;
-            m = mx;
-            ps[warp * KT + lane] = p;
-            if (lane == 0) corr[warp] = a;
-        }
-        __syncthreads();
-        for (int h = 0; h < HG; ++h) {
-            const float a = corr[h];
-            acc[h][0] *= a;
-            acc[h][1] *= a;
-        }
-        for (int kk = 0; kk < KT; ++kk) {
-            if (!seen[kk]) continue;
-            const float v0 = ks[kk * (KVW + 1) + t], v1 = ks[kk * (KVW + 1) + t + 256];
-            for (int h = 0; h < HG; ++h) {
-                acc[h][0] = fmaf(ps[h * KT + kk], v0, acc[h][0]);
-                acc[h][1] = fmaf(ps[h * KT + kk], v1, acc[h][1]);
-            }
+        if (lane == 0) {
+            const int nt = left > 0 ? blocks_of(a, b) : 1;
+            s.start_b = b;
+            s.start_u = (int)(off / nt);
+            s.start_t = (int)(off % nt);
+            s.left = left;
         }
     }
-    if (lane == 0) linv[warp] = l == 0.f ? 0.f : 1.f / l;
+    tc_fence_before();
     __syncthreads();
-    for (int h = 0; h < HG && h0 + h < Hq; ++h) {
-        __nv_bfloat16* o = out + ((int64_t)row * Hq + h0 + h) * DV;
-        o[t] = __float2bfloat16_rn(acc[h][0] * linv[h]);
-        o[t + 256] = __float2bfloat16_rn(acc[h][1] * linv[h]);
+    cluster_sync();
+    tc_fence_after();
+    pdl_trigger();
+    const uint32_t tmem = s.tmem_base;
+    Walk w;
+    w.start(a, s);
+
+    if (warp < SOFT_WARPS) {
+        // ------------------------------------------------ softmax, Q, epilogue
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const int grp = warp >> 2;                  // which 32 of a buffer's 64 columns
+        const int half = (warp >> 1) & 1;           // which 64 of the block's keys
+        const int row = (warp & 1) * 32 + lane;
+        const int kw = half * 2 + grp;              // which 32 of the block's keys
+        const int part = kw;                        // of the four threads of a row
+        const uint32_t q_bar = map_to_rank(smem_u32(&s.q_full), 0), p_bar = map_to_rank(smem_u32(&s.p_full), 0);
+        float* xl = reinterpret_cast<float*>(smem + OFF_XL);
+        uint8_t* p_hi = smem + OFF_P + row * 128;
+        const int sw = row & 7;
+        uint32_t j = 0;
+        Rows r{};
+        float sq = 0.f;
+        if (w.left > 0) {
+            r = unit_rows(a, w.b, w.u);
+            sq = convert_q(a, r, smem, rank, tmem, lane_base);
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(q_bar);
+        }
+        while (w.left > 0) {
+            const int n = w.count(), len = seq_len(a, w.b), ctx = len - a.Lq;
+            const bool dense = a.idx == nullptr;
+            const int m = (int)rank * HROWS + row;          // of the unit
+            unsigned long long mask = ~0ull;                // nodes that this row sees
+            if (dense && m < r.rows) {
+                const int i = (r.node0 + m) / a.Hq;
+                mask = a.tree ? __ldg(a.tree + (int64_t)w.b * a.Lq + i) : i >= 63 ? ~0ull : (2ull << i) - 1;
+            }
+            const float arow = sq * a.scale_log2;
+            const uint64_t a2 = f2(arow, arow);
+            float mref = -INFINITY, l = 0.f;
+            for (int x = 0; x < n; ++x, ++j) {
+                const uint32_t buf = j & 1, ph = (j >> 1) & 1;
+                const int s0 = (w.t + x) * NB;              // the block's first entry
+                warp_wait(&s.sc_full[buf], ph, status, abort, 5);
+                warp_wait(&s.s_full[buf], ph, status, abort, 6);
+                tc_fence_after();
+                uint32_t t[32];
+                tmem_ld32(tmem + lane_base + TM_S + 64 * buf + 32 * grp, t);
+                const float4* g4 = reinterpret_cast<const float4*>(smem + OFF_SC + buf * (3 * NB * 4)) + kw * 8;
+                uint32_t seen = reinterpret_cast<const uint32_t*>(smem + OFF_MASK)[buf * 4 + kw];
+                if (dense) seen &= tree_bits(mask, s0 + kw * 32 - ctx);
+                tmem_ld_wait();
+                float y[32];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float4 g = g4[c], lg = g4[NB / 4 + c];
+                    const float2 u = f2_split(ffma2(fmul2(f2(__uint_as_float(t[4 * c]), __uint_as_float(t[4 * c + 1])), a2),
+                                                    f2(g.x, g.y), f2(lg.x, lg.y)));
+                    const float2 v = f2_split(ffma2(fmul2(f2(__uint_as_float(t[4 * c + 2]), __uint_as_float(t[4 * c + 3])), a2),
+                                                    f2(g.z, g.w), f2(lg.z, lg.w)));
+                    y[4 * c] = u.x; y[4 * c + 1] = u.y; y[4 * c + 2] = v.x; y[4 * c + 3] = v.y;
+                }
+                if (seen != 0xffffffffu) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (!((seen >> c) & 1u)) y[c] = -INFINITY;
+                }
+                float mx = fmaxf(y[0], y[1]);
+#pragma unroll
+                for (int c = 2; c < 32; c += 2) mx = fmaxf(mx, fmaxf(y[c], y[c + 1]));
+                float* xm = reinterpret_cast<float*>(smem + OFF_XM) + buf * (4 * HROWS);
+                xm[part * HROWS + row] = mx;
+                soft_sync();
+                mx = fmaxf(fmaxf(xm[row], xm[HROWS + row]), fmaxf(xm[2 * HROWS + row], xm[3 * HROWS + row]));
+                const bool grow = mx > mref + SLACK;
+                const float mnew = grow ? mx : mref;
+                const float factor = grow ? ex2_approx(mref - mnew) : 1.f;   // 0 from -inf
+                const float off = mnew == -INFINITY ? 0.f : TOP - mnew;
+                const uint64_t off2 = f2(off, off);
+                uint64_t l2 = f2(0.f, 0.f);
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float4 ig = g4[2 * (NB / 4) + c];
+                    const float2 u = f2_split(fadd2(f2(y[4 * c], y[4 * c + 1]), off2));
+                    const float2 v = f2_split(fadd2(f2(y[4 * c + 2], y[4 * c + 3]), off2));
+                    const float e0 = ex2_approx(u.x), e1 = ex2_approx(u.y), e2 = ex2_approx(v.x), e3 = ex2_approx(v.y);
+                    l2 = ffma2(f2(e0, e1), f2(ig.x, ig.y), l2);
+                    l2 = ffma2(f2(e2, e3), f2(ig.z, ig.w), l2);
+                    uint32_t h0, h1, r0, r1;
+                    split_weights(e0, e1, h0, r0);
+                    split_weights(e2, e3, h1, r1);
+                    hi[c] = h0 | h1 << 16;
+                    lo[c] = r0 | r1 << 16;
+                }
+                const float2 ls = f2_split(l2);
+                l = l * factor + (ls.x + ls.y);
+                mref = mnew;
+                if (j > 0) warp_wait(&s.pv_done[buf ^ 1], ((j - 1) >> 1) & 1, status, abort, 7);
+                if (x > 0 && __any_sync(0xffffffffu, grow)) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t addr = tmem + lane_base + TM_O + 128 * grp + 32 * c;
+                        tmem_ld32(addr, t);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) t[i] = __float_as_uint(__uint_as_float(t[i]) * factor);
+                        tmem_st32(addr, t);
+                    }
+                    tmem_st_wait();
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int at = ((kw * 2 + c) ^ sw) << 4;
+                    *reinterpret_cast<uint4*>(p_hi + at) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+                    *reinterpret_cast<uint4*>(p_hi + ATOM + at) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                }
+                if (dense && s0 + NB > ctx) {
+                    // A node that some of the unit's rows see and others do
+                    // not: its NaN codes become 0 here, so that 0 weights
+                    // leave no NaN; the weights of the rows that see it are
+                    // NaN by themselves.
+                    warp_wait(&s.v_full[buf], ph, status, abort, 8);
+                    uint4* v = reinterpret_cast<uint4*>(smem + OFF_V + buf * V_STAGE) + threadIdx.x;
+                    for (int c = 0; c < V_STAGE / 16 / 256; ++c) {
+                        const uint4 o = v[c * 256];
+                        uint4 z = o;
+                        z.x &= ~__vcmpeq4(o.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        z.y &= ~__vcmpeq4(o.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        z.z &= ~__vcmpeq4(o.z & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        z.w &= ~__vcmpeq4(o.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        if (z.x != o.x || z.y != o.y || z.z != o.z || z.w != o.w) v[c * 256] = z;
+                    }
+                }
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(p_bar);
+            }
+            // the next unit's Q, then this unit's results
+            const Rows done = r;
+            const bool whole = w.t == 0 && n == w.nt;
+            const int slot = (blockIdx.x / 2) * 2 + (w.t > 0 ? 0 : 1);
+            w.next(a);
+            if (w.left > 0) {
+                r = unit_rows(a, w.b, w.u);
+                sq = convert_q(a, r, smem, rank, tmem, lane_base);
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(q_bar);
+            }
+            xl[part * HROWS + row] = l;
+            soft_sync();
+            l = (xl[row] + xl[HROWS + row]) + (xl[2 * HROWS + row] + xl[3 * HROWS + row]);
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const bool ok = warp_wait(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, status, abort, 9) && m < done.rows;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t t[32];
+                tmem_ld32(tmem + lane_base + TM_O + 128 * grp + 32 * c, t);
+                tmem_ld_wait();
+                const int col = 256 * grp + 128 * half + 32 * c;
+                if (whole) {
+                    uint4* o = reinterpret_cast<uint4*>(a.out + (done.first + m) * DV + col);
+                    if (ok) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                u[k] = bf16_pair(__uint_as_float(t[8 * i + 2 * k]) * inv, __uint_as_float(t[8 * i + 2 * k + 1]) * inv);
+                            o[i] = make_uint4(u[0], u[1], u[2], u[3]);
+                        }
+                    }
+                } else if (ok) {
+                    uint4* o = reinterpret_cast<uint4*>(a.part_o + ((int64_t)slot * MROWS + m) * DV + col);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = make_uint4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
+                }
+            }
+            if (!whole && ok && part == 0) a.part_ml[slot * MROWS + m] = make_float2(mref, l);
+            tc_fence_before();
+        }
+    } else if (warp == W_LOAD) {
+        // ------------------------------------------------ positions, tiles, scales
+        const int oob = a.num_pages * a.page_size;
+        uint32_t j = 0;
+        bool ok = true;
+        while (w.left > 0 && ok) {
+            const int n = w.count(), len = seq_len(a, w.b), ctx = len - a.Lq;
+            if (len == 0 && lane == 0) flag_status(status, IC_DEV_INDEX_RANGE);
+            const int64_t qrow = (int64_t)w.b * a.Lq + w.u;           // idx given: the unit's row
+            unsigned long long mask = ~0ull;
+            if (a.idx) mask = a.tree ? __ldg(a.tree + qrow) : w.u >= 63 ? ~0ull : (2ull << w.u) - 1;
+            const int32_t* table = a.block_table + (int64_t)w.b * a.max_pages;
+            for (int x = 0; x < n && ok; ++x, ++j) {
+                const uint32_t buf = j & 1;
+                int rows[4];
+                float g[4];
+                uint32_t valid = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = (w.t + x) * NB + lane * 4 + i;
+                    int p = a.idx ? (e < a.k ? __ldg(a.idx + qrow * a.k + e) : -1) : (e < len ? e : -1);
+                    if (p != -1 && (p < 0 || p >= len)) {
+                        if (len > 0) flag_status(status, IC_DEV_INDEX_RANGE);
+                        p = -1;
+                    }
+                    if (a.idx && p >= ctx && (p - ctx >= 64 || !((mask >> (p - ctx)) & 1))) p = -1;
+                    rows[i] = p;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int p = rows[i];
+                    int page = p >= 0 ? __ldg(table + p / a.page_size) : -1;
+                    if (p >= 0 && (page < 0 || page >= a.num_pages)) {
+                        flag_status(status, IC_DEV_INDEX_RANGE);
+                        page = -1;
+                    }
+                    rows[i] = page >= 0 ? page * a.page_size + p % a.page_size : oob;
+                    valid |= page >= 0 ? 1u << i : 0u;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) g[i] = (valid >> i) & 1 ? __ldg(a.kv_scale + rows[i]) : 1.f;
+                const bool box = a.idx == nullptr && __all_sync(0xffffffffu, valid == 15u);
+                const int row0 = __shfl_sync(0xffffffffu, rows[0], 0);
+
+                if (j >= 2) ok = warp_wait(&s.s_full[buf], ((j - 2) >> 1) & 1, status, abort, 1);
+                if (!ok) break;
+                uint32_t dst = sbase + OFF_K + buf * K_STAGE;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&s.k_full[buf], K_STAGE);
+                    if (box)
+                        for (int c = 0; c < 5; ++c)
+                            tma_load_2d(smem + OFF_K + buf * K_STAGE + c * ATOM, &map_box, &s.k_full[buf], c * 128,
+                                        row0 + HROWS * (int)rank);
+                }
+                __syncwarp();
+                if (!box && (uint32_t)(lane >> 4) == rank)
+                    for (int c = 0; c < 5; ++c)
+                        tma_gather4(dst + c * ATOM + (lane & 15) * 512, &map_rows, &s.k_full[buf], c * 128, rows[0],
+                                    rows[1], rows[2], rows[3]);
+                if (j >= 2) ok = warp_wait(&s.pv_done[buf], ((j - 2) >> 1) & 1, status, abort, 2);
+                if (!ok) break;
+                dst = sbase + OFF_V + buf * V_STAGE;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&s.v_full[buf], V_STAGE);
+                    if (box)
+                        for (int c = 0; c < 4; ++c)
+                            tma_load_2d(smem + OFF_V + buf * V_STAGE + c * ATOM, &map_box, &s.v_full[buf],
+                                        (c >> 1) * 256 + (int)rank * 128, row0 + (c & 1) * 64);
+                }
+                __syncwarp();
+                if (!box)
+                    for (int c = 0; c < 2; ++c)
+                        tma_gather4(dst + c * 2 * ATOM + lane * 512, &map_rows, &s.v_full[buf], c * 256 + (int)rank * 128,
+                                    rows[0], rows[1], rows[2], rows[3]);
+                float4* sc = reinterpret_cast<float4*>(smem + OFF_SC + buf * (3 * NB * 4)) + lane;
+                float lg[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t u = __float_as_uint(g[i]);
+                    lg[i] = (u & 0x807fffffu) == 0u && u != 0u ? (float)((int)(u >> 23) - 127) : log2f(g[i]);
+                }
+                sc[0] = make_float4(g[0], g[1], g[2], g[3]);
+                sc[NB / 4] = make_float4(lg[0], lg[1], lg[2], lg[3]);
+                sc[2 * (NB / 4)] = make_float4(1.f / g[0], 1.f / g[1], 1.f / g[2], 1.f / g[3]);
+                uint32_t word = valid << (4 * (lane & 7));
+                word |= __shfl_xor_sync(0xffffffffu, word, 1);
+                word |= __shfl_xor_sync(0xffffffffu, word, 2);
+                word |= __shfl_xor_sync(0xffffffffu, word, 4);
+                if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(smem + OFF_MASK)[buf * 4 + (lane >> 3)] = word;
+                mbar_arrive(&s.sc_full[buf]);
+            }
+            if (ok) w.next(a);
+        }
+        // own copies have landed before the CTA exits, whatever happened
+        for (uint32_t i = j > 2 ? j - 2 : 0; i < j; ++i) {
+            mbar_wait_drain(&s.k_full[i & 1], (i >> 1) & 1, 200000000ull);
+            mbar_wait_drain(&s.v_full[i & 1], (i >> 1) & 1, 200000000ull);
+        }
+        if (!ok) {                  // a block whose K was sent for and whose V was not
+            mbar_wait_drain(&s.k_full[j & 1], (j >> 1) & 1, 200000000ull);
+        }
+    } else if (rank == 0) {
+        // ------------------------------------------------ MMA issue
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_f32acc(0, 0, MROWS, NB), id_r = idesc_f32acc(1, 1, MROWS, NB);
+            constexpr uint32_t id_ph = idesc_f32acc(0, 0, MROWS, 256, 0, 1), id_pl = idesc_f32acc(1, 0, MROWS, 256, 0, 1);
+            const uint64_t qd = desc_sw128(sbase + OFF_Q, 16, 1024), kd = desc_sw128(sbase + OFF_K, 16, 1024);
+            const uint64_t vd = desc_sw128(sbase + OFF_V, 16, 1024), pd = desc_sw128(sbase + OFF_P, 16, 1024);
+            uint32_t unit = 0;
+            bool ok = true;
+            auto issue_s = [&](uint32_t j, bool first) {
+                const uint32_t buf = j & 1, ph = (j >> 1) & 1;
+                if (first) ok = ok && mbar_wait_cluster(&s.q_full, unit++ & 1, status, abort, 10);
+                ok = ok && mbar_wait(&s.k_full[buf], ph, status, abort, 11);
+                ok = ok && mbar_wait_cluster(&s.k_peer[buf], ph, status, abort, 12);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t d = tmem + TM_S + 64 * buf;
+                const uint64_t kb = kd + buf * (K_STAGE >> 4);
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    mma_f8_pair(d, qd + (c >> 2) * (ATOM >> 4) + (c & 3) * 2, kb + (c >> 2) * (ATOM >> 4) + (c & 3) * 2, id_s, c > 0);
+#pragma unroll
+                for (int c = 0; c < 12; ++c)
+                    mma_f8_pair(d, qd + (4 + (c >> 2)) * (ATOM >> 4) + (c & 3) * 2, kb + (c >> 2) * (ATOM >> 4) + (c & 3) * 2, id_s, 1);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mma_f8_ts_pair(d, tmem + TM_QL + 8 * c, kb + 3 * (ATOM >> 4) + c * 2, id_s, 1);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mma_bf16_ts_pair(d, tmem + TM_QR + 8 * c, kb + 4 * (ATOM >> 4) + c * 2, id_r, 1);
+                mma_commit_pair(&s.s_full[buf]);
+            };
+            auto issue_pv = [&](uint32_t j, bool first) {
+                const uint32_t buf = j & 1, ph = (j >> 1) & 1;
+                ok = ok && mbar_wait_cluster(&s.p_full, j & 1, status, abort, 13);
+                ok = ok && mbar_wait(&s.v_full[buf], ph, status, abort, 14);
+                ok = ok && mbar_wait_cluster(&s.v_peer[buf], ph, status, abort, 15);
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t vb = vd + buf * (V_STAGE >> 4);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {          // hi, lo
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)        // value columns 0-255, 256-511
+                        mma_f8_pair(tmem + TM_O + 128 * h, pd + (c >> 2) * (ATOM >> 4) + (c & 3) * 2,
+                                    vb + h * (2 * ATOM >> 4) + (c & 3) * (32 * 128 >> 4), c < 4 ? id_ph : id_pl,
+                                    c > 0 || !first);
+                }
+                mma_commit_pair(&s.pv_done[buf]);
+            };
+            uint32_t j = 0;
+            if (w.left > 0) issue_s(0, true);
+            while (w.left > 0 && ok) {
+                const int n = w.count();
+                for (int x = 0; x < n && ok; ++x, ++j) {
+                    if (x + 1 < n) issue_s(j + 1, false);
+                    issue_pv(j, x == 0);
+                }
+                w.next(a);
+                if (w.left > 0) issue_s(j, true);
+            }
+            mma_commit_pair(&s.drain);
+            mbar_wait_drain(&s.drain, 0, 200000000ull);
+        }
+    } else {
+        // ------------------------------------------------ rank 1: its tiles have landed
+        if (lane == 0) {
+            uint32_t j = 0;
+            bool ok = true;
+            for (long long left = w.left; left > 0 && ok; --left, ++j) {
+                const uint32_t buf = j & 1, ph = (j >> 1) & 1;
+                ok = mbar_wait(&s.k_full[buf], ph, status, abort, 17);
+                if (ok) mbar_arrive_remote(map_to_rank(smem_u32(&s.k_peer[buf]), 0));
+                ok = ok && mbar_wait(&s.v_full[buf], ph, status, abort, 18);
+                if (ok) mbar_arrive_remote(map_to_rank(smem_u32(&s.v_peer[buf]), 0));
+            }
+            mbar_wait_drain(&s.drain, 0, 400000000ull);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == W_MMA) {
+        tc_fence_after();
+        tmem_dealloc_pair<TMEM_COLS>(tmem);
     }
 }
 
-constexpr size_t SMEM = sizeof(float) * (HG * KVW + KT * (KVW + 1) + HG * KT + 2 * HG);
+// ------------------------------------------------------------------ joining partial results
+// out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the runs that share
+// a unit.  One CTA per 8 rows of a unit, one warp per row; units that one run
+// covered whole have nothing to join.
+__global__ void __launch_bounds__(256)
+tree_join_kernel(const __grid_constant__ Args a, int max_pairs) {
+    __shared__ long long range[3];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.x / a.units, u = blockIdx.x % a.units;
+    pdl_trigger();
+    pdl_wait();
+    if (warp == 0) {
+        const long long n = total_blocks(a);
+        long long begin = 0;
+        if (a.idx) {
+            begin = (long long)blockIdx.x * a.list_blocks;
+        } else {
+            for (int i = lane; i < b; i += 32) begin += blocks_of(a, i);
+            for (int o = 16; o; o >>= 1) begin += __shfl_xor_sync(0xffffffffu, begin, o);
+            begin = begin * a.units + (long long)u * blocks_of(a, b);
+        }
+        if (lane == 0) {
+            range[0] = n;
+            range[1] = begin;
+            range[2] = begin + blocks_of(a, b);
+        }
+    }
+    __syncthreads();
+    const long long n = range[0], begin = range[1], end = range[2];
+    const int P = pairs_of(n, max_pairs);
+    const int p0 = pair_with(n, P, begin), p1 = pair_with(n, P, end - 1);
+    if (p0 == p1) return;
+    const Rows r = unit_rows(a, b, u);
+    const int m = blockIdx.y * 8 + warp;
+    if (m >= r.rows) return;
+    // slot of run p: 0 where it continues the unit, 1 where the unit begins in it
+    float top = -INFINITY;
+    for (int p = p0; p <= p1; ++p) {
+        const int slot = 2 * p + (run_begin(n, P, p) > begin ? 0 : 1);
+        top = fmaxf(top, a.part_ml[slot * MROWS + m].x);
+    }
+    float4 o[4];
+    float l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = p0; p <= p1; ++p) {
+        const int slot = 2 * p + (run_begin(n, P, p) > begin ? 0 : 1);
+        const float2 ml = a.part_ml[slot * MROWS + m];
+        const float wgt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_approx(ml.x - top);
+        const float4* po = reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * MROWS + m) * DV) + lane;
+        l += wgt * ml.y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 v = po[32 * i];
+            o[i].x += wgt * v.x; o[i].y += wgt * v.y; o[i].z += wgt * v.z; o[i].w += wgt * v.w;
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint2* d = reinterpret_cast<uint2*>(a.out + (r.first + m) * DV) + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[32 * i] = make_uint2(bf16_pair(o[i].x * inv, o[i].y * inv), bf16_pair(o[i].z * inv, o[i].w * inv));
+}
+
+// ------------------------------------------------------------------ host side
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (fn == nullptr) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+    return fn;
+}
+
+bool make_map(CUtensorMap* map, const void* base, int64_t rows, int box_rows) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)ROW, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ROW};
+    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// What the host knows of the list of blocks: at most this many.
+struct Plan {
+    int units, list_blocks, pairs;
+    int64_t blocks;
+};
+Plan plan(const ic_paged_rows& pr, int k, int Hq) {
+    Plan p;
+    p.units = k ? pr.Lq : ceil_div(pr.Lq * Hq, MROWS);
+    p.list_blocks = k ? ceil_div(k, NB) : (int)ceil_div64(pr.T_max, NB);
+    p.blocks = (int64_t)pr.B * p.units * p.list_blocks;
+    p.pairs = (int)std::min<int64_t>(MAX_PAIRS, p.blocks);
+    return p;
+}
 
 }  // namespace
 
-size_t tree_attn_q8_scratch_bytes(const ic_paged_rows& pr, int k, int Hq) { return 0; }
+size_t tree_attn_q8_scratch_bytes(const ic_paged_rows& pr, int k, int Hq) {
+    return (size_t)plan(pr, k, Hq).pairs * 2 * MROWS * (DV * sizeof(float) + sizeof(float2));
+}
 
 ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_scale,
                               const int32_t* idx, int k, const uint64_t* tree, const ic_paged_rows& pr, int Hq, float scale,
                               void* out, uint32_t* status, void* scratch, cudaStream_t s) {
-    if ((int64_t)pr.B * pr.Lq > 0x7fffffffLL) return IC_ERR_UNSUPPORTED;
-    if (cudaFuncSetAttribute(tree_attn_simple_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)SMEM) != cudaSuccess)
+    const Plan p = plan(pr, k, Hq);
+    const int64_t all_units = (int64_t)pr.B * p.units;
+    if ((int64_t)pr.B * pr.Lq > 0x7fffffffLL || all_units > 0x7fffffffLL) return IC_ERR_UNSUPPORTED;
+    CUtensorMap map_rows, map_box;
+    const int64_t rows = (int64_t)pr.num_pages * pr.page_size;
+    if (!make_map(&map_rows, kv_q8, rows, 1) || !make_map(&map_box, kv_q8, rows, 64)) return cuda_error("tree_attn_q8");
+    Args a;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.kv_scale = kv_scale;
+    a.idx = idx;
+    a.tree = reinterpret_cast<const unsigned long long*>(tree);
+    a.seq_lens = pr.seq_lens;
+    a.block_table = pr.block_table;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.part_o = static_cast<float*>(scratch);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)p.pairs * 2 * MROWS * DV);
+    a.status = status;
+    a.k = k;
+    a.B = pr.B;
+    a.Lq = pr.Lq;
+    a.Hq = Hq;
+    a.T_max = pr.T_max;
+    a.max_pages = pr.max_pages;
+    a.page_size = pr.page_size;
+    a.num_pages = pr.num_pages;
+    a.units = p.units;
+    a.list_blocks = p.list_blocks;
+    a.scale_log2 = scale * LOG2E;
+    if (cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES) != cudaSuccess)
         return cuda_error("tree_attn_q8");
-    const int64_t rows = (int64_t)pr.B * pr.Lq;
-    if (launch_ex(tree_attn_simple_kernel, dim3((unsigned)rows, (unsigned)ceil_div(Hq, HG)), dim3(THREADS),
-                  SMEM, s, pdl_rows(rows), 0, static_cast<const __nv_bfloat16*>(q),
-                  static_cast<const uint8_t*>(kv_q8), kv_scale, idx, k,
-                  reinterpret_cast<const unsigned long long*>(tree), pr, Hq, scale,
-                  static_cast<__nv_bfloat16*>(out), status) != cudaSuccess)
+    const bool pdl = pdl_rows((int64_t)pr.B * pr.Lq);
+    if (launch_ex(tree_attn_kernel, dim3((unsigned)(2 * p.pairs)), dim3(THREADS), SMEM_BYTES, s, pdl, 0, map_rows, map_box,
+                  a) != cudaSuccess)
         return cuda_error("tree_attn_q8");
     count_launch(IC_LK_TREE);
+    ic_status st = last_launch_status();
+    // with lists the host knows the runs: every unit may be whole
+    const bool joins = !k || p.blocks % p.pairs != 0 || (p.blocks / p.pairs) % p.list_blocks != 0;
+    if (st != IC_OK || !joins) return st;
+    if (launch_ex(tree_join_kernel, dim3((unsigned)all_units, MROWS / 8), dim3(256), 0, s, pdl, 0, a, p.pairs) != cudaSuccess)
+        return cuda_error("tree_join");
+    count_launch(IC_LK_COMBINE);
     return last_launch_status();
 }
 

@@ -31,20 +31,23 @@
 // 64 of the block's 128 keys whole (for Q K^T) and half of the value columns
 // of all 128 (for P V): an M = 128 product of a pair takes its B operand in
 // two halves, split by keys for the one and by columns for the other.
-//   warps 0-7  softmax (thread = row x 32 keys), conversion of Q, epilogue
-//   warp 8     resolves positions to cache rows; TMA (one box per 64
-//              consecutive rows, four-row gathers otherwise; a row that
-//              nobody may see becomes an out-of-range row, which TMA fills
-//              with zeros); scales and masks of the block
-//   warp 9     rank 0: issues the MMAs: S(j+1) before P V(j), so that the
-//              softmax of a block runs under the next block's Q K^T;
-//              rank 1: tells rank 0 when its own tiles have landed
+//   warps 0-7   softmax (thread = row x 32 keys), conversion of Q, epilogue
+//   warps 8-11  copy the block's rows: 8 and 9 K, 10 and 11 V, 16 bytes a lane
+//               (cp.async, 128 adjacent bytes per row and eight lanes; a row
+//               that nobody may see is filled with zeros), or one TMA box per
+//               64 rows where a block is 128 consecutive rows
+//   warps 12-13 resolve positions to cache rows, scales and masks, a block
+//               each in turn, ahead of the copies (a ring of three blocks)
+//   warp 14     rank 0: issues the MMAs: S(j+1) before P V(j), so that the
+//               softmax of a block runs under the next block's Q K^T;
+//               rank 1: passes on that its own operands are in place
+//   warp 15     idle (it completes a warpgroup, for setmaxnreg)
 // Tensor memory: O 256 columns, two S buffers of 64, Q's bfloat16 columns 32,
 // one of Q's eight 8-bit slices 32.  Shared memory: seven slices of Q 56 KB,
-// K 2 x 40 KB, V 2 x 32 KB, P 16 KB.
+// K 2 x 40 KB, V 2 x 32 KB, P 16 KB, the ring 6 KB.
 //
-// Every wait is bounded (sm100.cuh); sites: 1-4 producer, 5-9 softmax, 10-16
-// MMA issuer, 17-18 relay.
+// Every wait is bounded (sm100.cuh); sites: 1-4 copies, 5-9 softmax, 10-15
+// MMA issue, 16 resolution.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -67,14 +70,25 @@ constexpr int OFF_Q = 0;
 constexpr int OFF_K = OFF_Q + Q_SMEM * ATOM;
 constexpr int OFF_V = OFF_K + 2 * K_STAGE;
 constexpr int OFF_P = OFF_V + 2 * V_STAGE;
-constexpr int OFF_SC = OFF_P + 2 * ATOM;      // [2][3][128] float: scale, its log2, its inverse
-constexpr int OFF_XM = OFF_SC + 2 * 3 * NB * 4;       // [2][4][64] float: row maxima
+constexpr int RING = 3;
+struct Info {                                 // one block, resolved
+    int rows[NB];                             // cache rows, -1: seen by nobody
+    uint32_t scale[NB];                       // bfloat16 pairs: log2 of the scale, the scale above it
+    uint32_t seen[NB / 32];                   // bit: not -1
+    int box;                                  // 128 consecutive cache rows from rows[0] on
+    int pad[3];
+};
+constexpr int OFF_INFO = OFF_P + 2 * ATOM;
+constexpr int OFF_XM = OFF_INFO + RING * (int)sizeof(Info);   // [2][4][64] float: row maxima
 constexpr int OFF_XL = OFF_XM + 2 * 4 * HROWS * 4;    // [4][64] float: row sums
 constexpr int OFF_SQ = OFF_XL + 4 * HROWS * 4;        // [64] float: scales of Q's rows
-constexpr int OFF_MASK = OFF_SQ + HROWS * 4;          // [2][4] uint32: seen positions of a block
-constexpr int OFF_BARS = OFF_MASK + 32;
-constexpr int SOFT_WARPS = 8, W_LOAD = 8, W_MMA = 9;
-constexpr int THREADS = 32 * 10;
+constexpr int OFF_BARS = OFF_SQ + HROWS * 4;
+constexpr int SOFT_WARPS = 8, W_COPY = 8, W_RES = 12, W_MMA = 14;
+constexpr int THREADS = 32 * 16;
+// Registers per thread after the warpgroups re-balance them: launched at 128,
+// the shares add up to the same total, 4 x 32 x (2 x 184 + 2 x 72) = 65536.
+constexpr int REGS_SMALL = 72, REGS_LARGE = 184;
+static_assert(4 * 32 * (2 * REGS_SMALL + 2 * REGS_LARGE) == THREADS * 128, "register shares");
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_QR = 384, TM_QL = 416;
 constexpr int TMEM_COLS = 512;
 constexpr int MAX_PAIRS = 74;                 // CTA pairs of 148 SMs
@@ -83,12 +97,13 @@ constexpr float TOP = 4.f, SLACK = 4.f;       // log2 of the largest weight when
                                               // set, and how far it may grow before O is rescaled
 
 struct __align__(8) Bars {
-    uint64_t q_full;                 // rank 0: Q of a unit is in place (both CTAs' warps)
+    uint64_t info_full[RING], info_free[RING];
+    uint64_t q_full;                 // Q of a unit is in place (own warps)
     uint64_t k_full[2], v_full[2];   // own tiles have landed
-    uint64_t k_peer[2], v_peer[2];   // rank 0: rank 1's tiles have landed
-    uint64_t sc_full[2];             // scales and masks of a block
+    uint64_t s_peer[2];              // rank 0: rank 1's K (and Q) are in place
     uint64_t s_full[2];              // S of a block is complete: K stage free
-    uint64_t p_full;                 // rank 0: P of a block is in place (both CTAs' warps)
+    uint64_t p_full;                 // P of a block is in place (own warps)
+    uint64_t pv_peer[2];             // rank 0: rank 1's P and V are in place
     uint64_t pv_done[2];             // P V of a block is complete: V stage, P free
     uint64_t drain;
     uint32_t tmem_base;
@@ -102,13 +117,14 @@ static_assert(SMEM_BYTES <= 232448 && OFF_BARS % 8 == 0, "shared memory budget")
 
 struct Args {
     const __nv_bfloat16* q;
+    const uint8_t* cache;
     const float* kv_scale;
     const int32_t* idx;
     const unsigned long long* tree;
     const int32_t* seq_lens;
     const int32_t* block_table;
     __nv_bfloat16* out;
-    float* part_o;      // [2 * pairs][128][512]
+    uint4* part_o;      // [2 * pairs][PART]: float32, in the order of the threads that hold them
     float2* part_ml;    // [2 * pairs][128]: running maximum, sum
     uint32_t* status;
     int k, B, Lq, Hq, T_max, max_pages, page_size, num_pages;
@@ -210,6 +226,9 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// 2^-n of a packed scale 2^n (its bfloat16 in the upper half).
+__device__ __forceinline__ float inverse_of(uint32_t packed) { return __uint_as_float(0x7f000000u - (packed & 0xffff0000u)); }
+
 // Two e4m3 numbers and two e5m2 numbers for what they leave of (a, b).
 __device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
     hi = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -246,16 +265,58 @@ __device__ __forceinline__ uint32_t tree_bits(unsigned long long mask, int off) 
     return (uint32_t)(mask << -off) | ((1u << -off) - 1u);
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {   // the rest of 16: zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// A partial result of a unit: O of one thread (row (warp & 1) * 32 + lane of
+// CTA rank) in 16-byte pieces i = 0..7 of 32 columns c = 0..3 from
+// part_col(warp, c) on, so that a warp writes and reads 512 adjacent bytes.
+constexpr int PART = MROWS * DV / 4;
+__device__ __forceinline__ int64_t part_at(int slot, int rank, int warp, int c, int i, int lane) {
+    return (int64_t)slot * PART + ((((rank * 8 + warp) * 4 + c) * 8 + i) * 32 + lane);
+}
+__device__ __forceinline__ int part_col(int warp, int c) { return 256 * (warp >> 2) + 128 * ((warp >> 1) & 1) + 32 * c; }
+
+// A warp's share of a tile: 4 * GROUPS rows (rows[], -1: zeros) of ATOMS x
+// 128 bytes, STEP bytes apart in the cache row, DST bytes apart in the tile;
+// row0 is the first row's place in the tile.
+template <int GROUPS, int ATOMS, int STEP, int DST>
+__device__ __forceinline__ void copy_rows(uint32_t dst, int row0, const uint8_t* cache, const int* rows, int lane) {
+    int src_row[GROUPS];
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) src_row[g] = rows[g * 4 + (lane >> 3)];
+    // rows g and g + 2 are 8 apart: the same place in the swizzle
+    const int r = row0 + (lane >> 3);
+    const uint32_t d0 = dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+    const uint32_t d1 = dst + (r + 4) * 128 + (((lane & 7) ^ ((r + 4) & 7)) << 4);
+    cache += (lane & 7) * 16;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+        const uint32_t bytes = src_row[g] >= 0 ? 16u : 0u;
+        const uint8_t* src = cache + (int64_t)max(src_row[g], 0) * ROW;
+#pragma unroll
+        for (int c = 0; c < ATOMS; ++c)
+            copy16((g & 1 ? d1 : d0) + (g >> 1) * 1024 + c * DST, src + c * STEP, bytes);
+    }
+    copy_commit();
+}
+
 // ------------------------------------------------------------------ Q of a unit
-// The 64 rows of this CTA, 256 threads.  Returns this thread's row's scale
-// (row = lane of the quadrant & 63).
-__device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t* smem, uint32_t rank,
-                                           uint32_t tmem, uint32_t lane_base) {
+// The 64 rows of this CTA, 256 threads: a warp takes 8 rows, a lane 16 of the
+// coded columns.  What goes to tensor memory (lane = row) passes through the
+// P tiles, which are free once P V of block j - 1 is complete.  Returns the
+// scale of this thread's row.
+__device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t* smem, Bars& s, uint32_t rank,
+                                           uint32_t tmem, uint32_t lane_base, uint32_t j) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* sq = reinterpret_cast<float*>(smem + OFF_SQ);
     const int64_t first = r.first + rank * HROWS;
     const int rows = r.rows - (int)rank * HROWS;
-    uint4 v[8][2];
+    uint4 v[8][2], rest[2];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int row = warp * 8 + i;
@@ -264,6 +325,13 @@ __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t
         v[i][0] = ok ? __ldg(p) : make_uint4(0u, 0u, 0u, 0u);
         v[i][1] = ok ? __ldg(p + 1) : make_uint4(0u, 0u, 0u, 0u);
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = warp * 8 + i * 4 + (lane >> 3);
+        rest[i] = row < rows ? __ldg(reinterpret_cast<const uint4*>(a.q + (first + row) * KVW + DV) + (lane & 7))
+                             : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (j > 0) warp_wait(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, a.status, &s.abort, 8);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int row = warp * 8 + i;
@@ -283,46 +351,45 @@ __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t
             lo[2 * h] = low4(x, hi[2 * h]);
             lo[2 * h + 1] = low4(y, hi[2 * h + 1]);
         }
-        uint8_t* d = smem + OFF_Q + (lane >> 3) * ATOM + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
-        *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (lane < 24) *reinterpret_cast<uint4*>(d + 4 * ATOM) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        const int at = row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4*>(smem + OFF_Q + (lane >> 3) * ATOM + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(smem + (lane < 24 ? OFF_Q + (4 + (lane >> 3)) * ATOM : OFF_P) + at) =
+            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = warp * 8 + i * 4 + (lane >> 3);
+        const float inv = 1.f / sq[row];
+        const uint32_t u[4] = {rest[i].x, rest[i].y, rest[i].z, rest[i].w};
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            w[k] = bf16_pair(__uint_as_float(u[k] << 16) * inv, __uint_as_float(u[k] & 0xffff0000u) * inv);
+        *reinterpret_cast<uint4*>(smem + OFF_P + ATOM + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
     }
     soft_sync();
-    // tensor memory: the bfloat16 columns (warps 0-3), the last slice of lo (warps 4-7)
+    // to tensor memory: the last slice of lo (warps 4-7), the bfloat16 columns (warps 0-3)
     const int row = (warp & 1) * 32 + lane;
-    const float scale = sq[row], inv = 1.f / scale;
-    const bool ok = row < rows;
     uint32_t w[32];
-    if (warp < 4) {
-        const uint4* p = reinterpret_cast<const uint4*>(a.q + (first + row) * KVW + DV);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint4 x = ok ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[4 * i + j] = bf16_pair(__uint_as_float(u[j] << 16) * inv, __uint_as_float(u[j] & 0xffff0000u) * inv);
-        }
-        tmem_st32(tmem + lane_base + TM_QR, w);
-    } else {
-        const uint4* p = reinterpret_cast<const uint4*>(a.q + (first + row) * KVW + 384);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint4 x = ok ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
-            const float4 y = scaled4(x.x, x.y, inv), z = scaled4(x.z, x.w, inv);
-            w[2 * i] = low4(y, high4(y));
-            w[2 * i + 1] = low4(z, high4(z));
-        }
-        tmem_st32(tmem + lane_base + TM_QL, w);
+    for (int c = 0; c < 8; ++c) {
+        const uint4 x = *reinterpret_cast<const uint4*>(smem + OFF_P + (warp < 4 ? ATOM : 0) + row * 128 + ((c ^ (row & 7)) << 4));
+        w[4 * c] = x.x; w[4 * c + 1] = x.y; w[4 * c + 2] = x.z; w[4 * c + 3] = x.w;
     }
+    tmem_st32(tmem + lane_base + (warp < 4 ? TM_QR : TM_QL), w);
     tmem_st_wait();
-    return scale;
+    fence_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.q_full);
+    return sq[row];
 }
 
 // ------------------------------------------------------------------ the kernel
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-tree_attn_kernel(const __grid_constant__ CUtensorMap map_rows,    // box: 1 row x 128 bytes
-                 const __grid_constant__ CUtensorMap map_box,     // box: 64 rows x 128 bytes
+tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 rows x 128 bytes
                  const __grid_constant__ Args a) {
     extern __shared__ __align__(16) uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -334,26 +401,28 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_rows,    // box: 1 row 
     uint32_t* status = a.status;
 
     if (threadIdx.x == 0) {
-        mbar_init(&s.q_full, 2 * SOFT_WARPS);
-        mbar_init(&s.p_full, 2 * SOFT_WARPS);
+        mbar_init(&s.q_full, SOFT_WARPS);
+        mbar_init(&s.p_full, SOFT_WARPS);
         mbar_init(&s.drain, 1);
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(&s.info_full[i], 1);
+            mbar_init(&s.info_free[i], SOFT_WARPS + 4);
+        }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.k_full[i], 1);
-            mbar_init(&s.v_full[i], 1);
-            mbar_init(&s.k_peer[i], 1);
-            mbar_init(&s.v_peer[i], 1);
-            mbar_init(&s.sc_full[i], 32);
+            mbar_init(&s.k_full[i], 2);
+            mbar_init(&s.v_full[i], 2);
+            mbar_init(&s.s_peer[i], 1);
+            mbar_init(&s.pv_peer[i], 1);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.pv_done[i], 1);
         }
         s.abort = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&map_rows);
         tma_prefetch_desc(&map_box);
     }
     if (warp == W_MMA) tmem_alloc_pair<TMEM_COLS>(&s.tmem_base);
     pdl_wait();
-    if (warp == W_LOAD) {            // this pair's run
+    if (warp == W_RES) {             // this pair's run
         const long long n = total_blocks(a);
         const int P = pairs_of(n, gridDim.x / 2), p = blockIdx.x / 2;
         long long begin = 0, left = 0;
@@ -398,10 +467,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_rows,    // box: 1 row 
     cluster_sync();
     tc_fence_after();
     pdl_trigger();
-    const uint32_t tmem = s.tmem_base;
+    const uint32_t tmem = 0;             // all of the tensor memory was allocated: it begins at column 0
     Walk w;
     w.start(a, s);
 
+    if (warp < SOFT_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REGS_LARGE) : "memory");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_SMALL) : "memory");
     if (warp < SOFT_WARPS) {
         // ------------------------------------------------ softmax, Q, epilogue
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -410,20 +481,15 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_rows,    // box: 1 row 
         const int row = (warp & 1) * 32 + lane;
         const int kw = half * 2 + grp;              // which 32 of the block's keys
         const int part = kw;                        // of the four threads of a row
-        const uint32_t q_bar = map_to_rank(smem_u32(&s.q_full), 0), p_bar = map_to_rank(smem_u32(&s.p_full), 0);
         float* xl = reinterpret_cast<float*>(smem + OFF_XL);
         uint8_t* p_hi = smem + OFF_P + row * 128;
         const int sw = row & 7;
-        uint32_t j = 0;
+        uint32_t j = 0, slot = 0, turn = 0;         // block j is use `turn` of ring slot `slot`
         Rows r{};
         float sq = 0.f;
         if (w.left > 0) {
             r = unit_rows(a, w.b, w.u);
-            sq = convert_q(a, r, smem, rank, tmem, lane_base);
-            fence_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(q_bar);
+            sq = convert_q(a, r, smem, s, rank, tmem, lane_base, 0);
         }
         while (w.left > 0) {
             const int n = w.count(), len = seq_len(a, w.b), ctx = len - a.Lq;
@@ -440,24 +506,30 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_rows,    // box: 1 row 
             for (int x = 0; x < n; ++x, ++j) {
                 const uint32_t buf = j & 1, ph = (j >> 1) & 1;
                 const int s0 = (w.t + x) * NB;              // the block's first entry
-                warp_wait(&s.sc_full[buf], ph, status, abort, 5);
+                warp_wait(&s.info_full[slot], turn & 1, status, abort, 5);
+                const Info& info = reinterpret_cast<const Info*>(smem + OFF_INFO)[slot];
                 warp_wait(&s.s_full[buf], ph, status, abort, 6);
                 tc_fence_after();
                 uint32_t t[32];
                 tmem_ld32(tmem + lane_base + TM_S + 64 * buf + 32 * grp, t);
-                const float4* g4 = reinterpret_cast<const float4*>(smem + OFF_SC + buf * (3 * NB * 4)) + kw * 8;
-                uint32_t seen = reinterpret_cast<const uint32_t*>(smem + OFF_MASK)[buf * 4 + kw];
+                const uint4* g4 = reinterpret_cast<const uint4*>(info.scale) + kw * 8;
+                uint32_t seen = info.seen[kw];
                 if (dense) seen &= tree_bits(mask, s0 + kw * 32 - ctx);
+                uint32_t g[32];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 x = g4[c];
+                    g[4 * c] = x.x; g[4 * c + 1] = x.y; g[4 * c + 2] = x.z; g[4 * c + 3] = x.w;
+                }
                 tmem_ld_wait();
                 float y[32];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float4 g = g4[c], lg = g4[NB / 4 + c];
-                    const float2 u = f2_split(ffma2(fmul2(f2(__uint_as_float(t[4 * c]), __uint_as_float(t[4 * c + 1])), a2),
-                                                    f2(g.x, g.y), f2(lg.x, lg.y)));
-                    const float2 v = f2_split(ffma2(fmul2(f2(__uint_as_float(t[4 * c + 2]), __uint_as_float(t[4 * c + 3])), a2),
-                                                    f2(g.z, g.w), f2(lg.z, lg.w)));
-                    y[4 * c] = u.x; y[4 * c + 1] = u.y; y[4 * c + 2] = v.x; y[4 * c + 3] = v.y;
+                for (int c = 0; c < 32; c += 2) {
+                    const float2 u = f2_split(ffma2(fmul2(f2(__uint_as_float(t[c]), __uint_as_float(t[c + 1])), a2),
+                                                    f2(__uint_as_float(g[c] & 0xffff0000u), __uint_as_float(g[c + 1] & 0xffff0000u)),
+                                                    f2(__uint_as_float(g[c] << 16), __uint_as_float(g[c + 1] << 16))));
+                    y[c] = u.x;
+                    y[c + 1] = u.y;
                 }
                 if (seen != 0xffffffffu) {
 #pragma unroll
@@ -479,21 +551,23 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_rows,    // box: 1 row 
                 uint64_t l2 = f2(0.f, 0.f);
                 uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float4 ig = g4[2 * (NB / 4) + c];
-                    const float2 u = f2_split(fadd2(f2(y[4 * c], y[4 * c + 1]), off2));
-                    const float2 v = f2_split(fadd2(f2(y[4 * c + 2], y[4 * c + 3]), off2));
+                for (int c = 0; c < 32; c += 4) {
+                    const float2 u = f2_split(fadd2(f2(y[c], y[c + 1]), off2));
+                    const float2 v = f2_split(fadd2(f2(y[c + 2], y[c + 3]), off2));
                     const float e0 = ex2_approx(u.x), e1 = ex2_approx(u.y), e2 = ex2_approx(v.x), e3 = ex2_approx(v.y);
-                    l2 = ffma2(f2(e0, e1), f2(ig.x, ig.y), l2);
-                    l2 = ffma2(f2(e2, e3), f2(ig.z, ig.w), l2);
+                    l2 = ffma2(f2(e0, e1), f2(inverse_of(g[c]), inverse_of(g[c + 1])), l2);
+                    l2 = ffma2(f2(e2, e3), f2(inverse_of(g[c + 2]), inverse_of(g[c + 3])), l2);
                     uint32_t h0, h1, r0, r1;
                     split_weights(e0, e1, h0, r0);
                     split_weights(e2, e3, h1, r1);
-                    hi[c] = h0 | h1 << 16;
-                    lo[c] = r0 | r1 << 16;
+                    hi[c / 4] = h0 | h1 << 16;
+                    lo[c / 4] = r0 | r1 << 16;
                 }
                 const float2 ls = f2_split(l2);
                 l = l * factor + (ls.x + ls.y);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.info_free[slot]);
+                if (++slot == RING) { slot = 0; ++turn; }
                 mref = mnew;
                 if (j > 0) warp_wait(&s.pv_done[buf ^ 1], ((j - 1) >> 1) & 1, status, abort, 7);
                 if (x > 0 && __any_sync(0xffffffffu, grow)) {
@@ -535,57 +609,119 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_rows,    // box: 1 row 
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(p_bar);
+                if (lane == 0) mbar_arrive(&s.p_full);
             }
             // the next unit's Q, then this unit's results
             const Rows done = r;
             const bool whole = w.t == 0 && n == w.nt;
-            const int slot = (blockIdx.x / 2) * 2 + (w.t > 0 ? 0 : 1);
+            const int part_slot = (blockIdx.x / 2) * 2 + (w.t > 0 ? 0 : 1);
             w.next(a);
             if (w.left > 0) {
                 r = unit_rows(a, w.b, w.u);
-                sq = convert_q(a, r, smem, rank, tmem, lane_base);
-                fence_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(q_bar);
+                sq = convert_q(a, r, smem, s, rank, tmem, lane_base, j);
             }
             xl[part * HROWS + row] = l;
             soft_sync();
             l = (xl[row] + xl[HROWS + row]) + (xl[2 * HROWS + row] + xl[3 * HROWS + row]);
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const bool ok = warp_wait(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, status, abort, 9) && m < done.rows;
+            const bool ok = warp_wait(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, status, abort, 9);
             tc_fence_after();
+            uint8_t* stage = smem + OFF_P + warp * 2048;       // 32 rows x 64 bytes
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t t[32];
                 tmem_ld32(tmem + lane_base + TM_O + 128 * grp + 32 * c, t);
                 tmem_ld_wait();
-                const int col = 256 * grp + 128 * half + 32 * c;
                 if (whole) {
-                    uint4* o = reinterpret_cast<uint4*>(a.out + (done.first + m) * DV + col);
-                    if (ok) {
+                    // through shared memory, so that four lanes write 64 adjacent bytes of a row
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t u[4];
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t u[4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                u[k] = bf16_pair(__uint_as_float(t[8 * i + 2 * k]) * inv, __uint_as_float(t[8 * i + 2 * k + 1]) * inv);
-                            o[i] = make_uint4(u[0], u[1], u[2], u[3]);
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            u[k] = bf16_pair(__uint_as_float(t[8 * i + 2 * k]) * inv, __uint_as_float(t[8 * i + 2 * k + 1]) * inv);
+                        *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
-                } else if (ok) {
-                    uint4* o = reinterpret_cast<uint4*>(a.part_o + ((int64_t)slot * MROWS + m) * DV + col);
+                    __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = make_uint4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = 8 * i + (lane >> 2), mm = (int)rank * HROWS + (warp & 1) * 32 + rr;
+                        const uint4 o = *reinterpret_cast<const uint4*>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+                        if (ok && mm < done.rows)
+                            *(reinterpret_cast<uint4*>(a.out + (done.first + mm) * DV + part_col(warp, c)) + (lane & 3)) = o;
+                    }
+                    __syncwarp();
+                } else if (ok) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        a.part_o[part_at(part_slot, rank, warp, c, i, lane)] = make_uint4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
                 }
             }
-            if (!whole && ok && part == 0) a.part_ml[slot * MROWS + m] = make_float2(mref, l);
+            if (!whole && ok && part == 0) a.part_ml[part_slot * MROWS + m] = make_float2(mref, l);
             tc_fence_before();
         }
-    } else if (warp == W_LOAD) {
-        // ------------------------------------------------ positions, tiles, scales
-        const int oob = a.num_pages * a.page_size;
+    } else if (warp < W_RES) {
+        // ------------------------------------------------ copies of the tiles
+        // K: this CTA's 64 keys whole, 32 rows per warp; V: its columns of all
+        // keys, 64 rows per warp.  A block's copies are waited for after the
+        // next block's are sent: K(j + 1) is sent when S(j - 1) is complete,
+        // which is before S(j) can begin, and V alike.
+        const bool is_k = warp < W_COPY + 2;
+        const int mine = (warp - W_COPY) & 1;
+        const int stage_bytes = is_k ? K_STAGE : V_STAGE;
+        const uint32_t stage0 = sbase + (is_k ? OFF_K : OFF_V);
+        uint64_t* full = is_k ? s.k_full : s.v_full;
+        uint64_t* freed = is_k ? s.s_full : s.pv_done;
+        uint32_t j = 0, slot = 0, turn = 0;
+        bool ok = true, pending = false;
+        for (long long left = w.left; left > 0; --left, ++j) {
+            const uint32_t buf = j & 1;
+            ok = warp_wait(&s.info_full[slot], turn & 1, status, abort, 1);
+            if (ok && j >= 2) ok = warp_wait(&freed[buf], ((j - 2) >> 1) & 1, status, abort, is_k ? 2 : 3);
+            if (!ok) break;
+            const Info& info = reinterpret_cast<const Info*>(smem + OFF_INFO)[slot];
+            const uint32_t dst0 = stage0 + buf * stage_bytes;
+            const bool box = info.box != 0;
+            if (box) {
+                if (lane == 0 && mine == 0) {
+                    mbar_arrive_expect_tx(&full[buf], stage_bytes);
+                    uint8_t* d = smem + (dst0 - sbase);
+                    if (is_k)
+                        for (int c = 0; c < 5; ++c)
+                            tma_load_2d(d + c * ATOM, &map_box, &full[buf], c * 128, info.rows[0] + HROWS * (int)rank);
+                    else
+                        for (int c = 0; c < 4; ++c)
+                            tma_load_2d(d + c * ATOM, &map_box, &full[buf], (c >> 1) * 256 + (int)rank * 128,
+                                        info.rows[0] + (c & 1) * 64);
+                } else if (lane == 0) {
+                    mbar_arrive(&full[buf]);
+                }
+            } else {
+                if (is_k) copy_rows<8, 5, 128, ATOM>(dst0, mine * 32, a.cache, info.rows + (int)rank * HROWS + mine * 32, lane);
+                else copy_rows<16, 2, 256, 2 * ATOM>(dst0, mine * 64, a.cache + rank * 128, info.rows + mine * 64, lane);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.info_free[slot]);
+            if (++slot == RING) { slot = 0; ++turn; }
+            if (pending) {
+                if (box) copy_wait<0>();
+                else copy_wait<1>();
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[buf ^ 1]);
+            }
+            pending = !box;
+        }
+        copy_wait<0>();
+        if (pending && ok) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[(j - 1) & 1]);
+        }
+        // boxes have landed before the CTA exits, whatever happened
+        for (uint32_t i = j > 2 ? j - 2 : 0; i < j; ++i) mbar_wait_drain(&full[i & 1], (i >> 1) & 1, 200000000ull);
+    } else if (warp < W_MMA) {
+        // ------------------------------------------------ positions, scales, masks
         uint32_t j = 0;
         bool ok = true;
         while (w.left > 0 && ok) {
@@ -596,14 +732,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_rows,    // box: 1 row 
             if (a.idx) mask = a.tree ? __ldg(a.tree + qrow) : w.u >= 63 ? ~0ull : (2ull << w.u) - 1;
             const int32_t* table = a.block_table + (int64_t)w.b * a.max_pages;
             for (int x = 0; x < n && ok; ++x, ++j) {
-                const uint32_t buf = j & 1;
+                if ((j & 1) != (uint32_t)(warp - W_RES)) continue;
                 int rows[4];
                 float g[4];
                 uint32_t valid = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int e = (w.t + x) * NB + lane * 4 + i;
-                    int p = a.idx ? (e < a.k ? __ldg(a.idx + qrow * a.k + e) : -1) : (e < len ? e : -1);
+                    rows[i] = a.idx ? (e < a.k ? __ldg(a.idx + qrow * a.k + e) : -1) : (e < len ? e : -1);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    int p = rows[i];
                     if (p != -1 && (p < 0 || p >= len)) {
                         if (len > 0) flag_status(status, IC_DEV_INDEX_RANGE);
                         p = -1;
@@ -611,155 +751,135 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_rows,    // box: 1 row 
                     if (a.idx && p >= ctx && (p - ctx >= 64 || !((mask >> (p - ctx)) & 1))) p = -1;
                     rows[i] = p;
                 }
+                int page[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) page[i] = rows[i] >= 0 ? __ldg(table + rows[i] / a.page_size) : -1;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int p = rows[i];
-                    int page = p >= 0 ? __ldg(table + p / a.page_size) : -1;
-                    if (p >= 0 && (page < 0 || page >= a.num_pages)) {
+                    if (rows[i] >= 0 && (page[i] < 0 || page[i] >= a.num_pages)) {
                         flag_status(status, IC_DEV_INDEX_RANGE);
-                        page = -1;
+                        page[i] = -1;
                     }
-                    rows[i] = page >= 0 ? page * a.page_size + p % a.page_size : oob;
-                    valid |= page >= 0 ? 1u << i : 0u;
+                    rows[i] = page[i] >= 0 ? page[i] * a.page_size + rows[i] % a.page_size : -1;
+                    valid |= page[i] >= 0 ? 1u << i : 0u;
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) g[i] = (valid >> i) & 1 ? __ldg(a.kv_scale + rows[i]) : 1.f;
+                for (int i = 0; i < 4; ++i) g[i] = rows[i] >= 0 ? __ldg(a.kv_scale + rows[i]) : 1.f;
                 const bool box = a.idx == nullptr && __all_sync(0xffffffffu, valid == 15u);
-                const int row0 = __shfl_sync(0xffffffffu, rows[0], 0);
-
-                if (j >= 2) ok = warp_wait(&s.s_full[buf], ((j - 2) >> 1) & 1, status, abort, 1);
-                if (!ok) break;
-                uint32_t dst = sbase + OFF_K + buf * K_STAGE;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&s.k_full[buf], K_STAGE);
-                    if (box)
-                        for (int c = 0; c < 5; ++c)
-                            tma_load_2d(smem + OFF_K + buf * K_STAGE + c * ATOM, &map_box, &s.k_full[buf], c * 128,
-                                        row0 + HROWS * (int)rank);
-                }
-                __syncwarp();
-                if (!box && (uint32_t)(lane >> 4) == rank)
-                    for (int c = 0; c < 5; ++c)
-                        tma_gather4(dst + c * ATOM + (lane & 15) * 512, &map_rows, &s.k_full[buf], c * 128, rows[0],
-                                    rows[1], rows[2], rows[3]);
-                if (j >= 2) ok = warp_wait(&s.pv_done[buf], ((j - 2) >> 1) & 1, status, abort, 2);
-                if (!ok) break;
-                dst = sbase + OFF_V + buf * V_STAGE;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&s.v_full[buf], V_STAGE);
-                    if (box)
-                        for (int c = 0; c < 4; ++c)
-                            tma_load_2d(smem + OFF_V + buf * V_STAGE + c * ATOM, &map_box, &s.v_full[buf],
-                                        (c >> 1) * 256 + (int)rank * 128, row0 + (c & 1) * 64);
-                }
-                __syncwarp();
-                if (!box)
-                    for (int c = 0; c < 2; ++c)
-                        tma_gather4(dst + c * 2 * ATOM + lane * 512, &map_rows, &s.v_full[buf], c * 256 + (int)rank * 128,
-                                    rows[0], rows[1], rows[2], rows[3]);
-                float4* sc = reinterpret_cast<float4*>(smem + OFF_SC + buf * (3 * NB * 4)) + lane;
-                float lg[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t u = __float_as_uint(g[i]);
-                    lg[i] = (u & 0x807fffffu) == 0u && u != 0u ? (float)((int)(u >> 23) - 127) : log2f(g[i]);
-                }
-                sc[0] = make_float4(g[0], g[1], g[2], g[3]);
-                sc[NB / 4] = make_float4(lg[0], lg[1], lg[2], lg[3]);
-                sc[2 * (NB / 4)] = make_float4(1.f / g[0], 1.f / g[1], 1.f / g[2], 1.f / g[3]);
                 uint32_t word = valid << (4 * (lane & 7));
                 word |= __shfl_xor_sync(0xffffffffu, word, 1);
                 word |= __shfl_xor_sync(0xffffffffu, word, 2);
                 word |= __shfl_xor_sync(0xffffffffu, word, 4);
-                if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(smem + OFF_MASK)[buf * 4 + (lane >> 3)] = word;
-                mbar_arrive(&s.sc_full[buf]);
+                uint32_t packed[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t u = __float_as_uint(g[i]) & 0x7f800000u;      // a power of two
+                    packed[i] = u | __float_as_uint((float)((int)(u >> 23) - 127)) >> 16;
+                }
+                const uint32_t slot = j % RING, turn = j / RING;
+                if (turn > 0) ok = warp_wait(&s.info_free[slot], (turn - 1) & 1, status, abort, 16);
+                if (!ok) break;
+                Info& info = reinterpret_cast<Info*>(smem + OFF_INFO)[slot];
+                reinterpret_cast<int4*>(info.rows)[lane] = make_int4(rows[0], rows[1], rows[2], rows[3]);
+                reinterpret_cast<uint4*>(info.scale)[lane] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+                if ((lane & 7) == 0) info.seen[lane >> 3] = word;
+                if (lane == 0) info.box = box;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.info_full[slot]);
             }
             if (ok) w.next(a);
         }
-        // own copies have landed before the CTA exits, whatever happened
-        for (uint32_t i = j > 2 ? j - 2 : 0; i < j; ++i) {
-            mbar_wait_drain(&s.k_full[i & 1], (i >> 1) & 1, 200000000ull);
-            mbar_wait_drain(&s.v_full[i & 1], (i >> 1) & 1, 200000000ull);
-        }
-        if (!ok) {                  // a block whose K was sent for and whose V was not
-            mbar_wait_drain(&s.k_full[j & 1], (j >> 1) & 1, 200000000ull);
-        }
-    } else if (rank == 0) {
-        // ------------------------------------------------ MMA issue
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_f32acc(0, 0, MROWS, NB), id_r = idesc_f32acc(1, 1, MROWS, NB);
-            constexpr uint32_t id_ph = idesc_f32acc(0, 0, MROWS, 256, 0, 1), id_pl = idesc_f32acc(1, 0, MROWS, 256, 0, 1);
-            const uint64_t qd = desc_sw128(sbase + OFF_Q, 16, 1024), kd = desc_sw128(sbase + OFF_K, 16, 1024);
-            const uint64_t vd = desc_sw128(sbase + OFF_V, 16, 1024), pd = desc_sw128(sbase + OFF_P, 16, 1024);
-            uint32_t unit = 0;
-            bool ok = true;
-            auto issue_s = [&](uint32_t j, bool first) {
-                const uint32_t buf = j & 1, ph = (j >> 1) & 1;
-                if (first) ok = ok && mbar_wait_cluster(&s.q_full, unit++ & 1, status, abort, 10);
-                ok = ok && mbar_wait(&s.k_full[buf], ph, status, abort, 11);
-                ok = ok && mbar_wait_cluster(&s.k_peer[buf], ph, status, abort, 12);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t d = tmem + TM_S + 64 * buf;
+    } else if (warp == W_MMA) {
+        // ------------------------------------------------ MMA issue; rank 1 passes its readiness on
+        // (counts and outcomes of waits go through votes, which keeps the
+        // control flow uniform)
+        constexpr uint32_t id_s = idesc_f32acc(0, 0, MROWS, NB), id_r = idesc_f32acc(1, 1, MROWS, NB);
+        constexpr uint32_t id_ph = idesc_f32acc(0, 0, MROWS, 256, 0, 1), id_pl = idesc_f32acc(1, 0, MROWS, 256, 0, 1);
+        const uint64_t qd = desc_sw128(sbase + OFF_Q, 16, 1024), kd = desc_sw128(sbase + OFF_K, 16, 1024);
+        const uint64_t vd = desc_sw128(sbase + OFF_V, 16, 1024), pd = desc_sw128(sbase + OFF_P, 16, 1024);
+        const uint32_t s_peer = map_to_rank(smem_u32(&s.s_peer[0]), 0), pv_peer = map_to_rank(smem_u32(&s.pv_peer[0]), 0);
+        const bool leader = __any_sync(0xffffffffu, rank == 0);
+        auto lane0_wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+            bool good = true;
+            if (lane == 0) good = mbar_wait(bar, parity, status, abort, site);
+            return __all_sync(0xffffffffu, good) != 0;
+        };
+        auto lane0_wait_peer = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+            bool good = true;
+            if (lane == 0) good = mbar_wait_cluster(bar, parity, status, abort, site);
+            return __all_sync(0xffffffffu, good) != 0;
+        };
+        uint32_t unit = 0;
+        bool ok = true;
+        auto issue_s = [&](uint32_t j, bool first) {
+            const uint32_t buf = j & 1, ph = (j >> 1) & 1;
+            if (first) ok = ok && lane0_wait(&s.q_full, unit++ & 1, 10);
+            ok = ok && lane0_wait(&s.k_full[buf], ph, 11);
+            if (!ok) return;
+            if (!leader) {
+                if (lane == 0) mbar_arrive_remote(s_peer + 8 * buf);
+                return;
+            }
+            ok = lane0_wait_peer(&s.s_peer[buf], ph, 12);
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t d = TM_S + 64 * buf;
                 const uint64_t kb = kd + buf * (K_STAGE >> 4);
-#pragma unroll
+#pragma unroll 4
                 for (int c = 0; c < 16; ++c)
                     mma_f8_pair(d, qd + (c >> 2) * (ATOM >> 4) + (c & 3) * 2, kb + (c >> 2) * (ATOM >> 4) + (c & 3) * 2, id_s, c > 0);
-#pragma unroll
+#pragma unroll 4
                 for (int c = 0; c < 12; ++c)
                     mma_f8_pair(d, qd + (4 + (c >> 2)) * (ATOM >> 4) + (c & 3) * 2, kb + (c >> 2) * (ATOM >> 4) + (c & 3) * 2, id_s, 1);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) mma_f8_ts_pair(d, tmem + TM_QL + 8 * c, kb + 3 * (ATOM >> 4) + c * 2, id_s, 1);
+                for (int c = 0; c < 4; ++c) mma_f8_ts_pair(d, TM_QL + 8 * c, kb + 3 * (ATOM >> 4) + c * 2, id_s, 1);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) mma_bf16_ts_pair(d, tmem + TM_QR + 8 * c, kb + 4 * (ATOM >> 4) + c * 2, id_r, 1);
+                for (int c = 0; c < 4; ++c) mma_bf16_ts_pair(d, TM_QR + 8 * c, kb + 4 * (ATOM >> 4) + c * 2, id_r, 1);
                 mma_commit_pair(&s.s_full[buf]);
-            };
-            auto issue_pv = [&](uint32_t j, bool first) {
-                const uint32_t buf = j & 1, ph = (j >> 1) & 1;
-                ok = ok && mbar_wait_cluster(&s.p_full, j & 1, status, abort, 13);
-                ok = ok && mbar_wait(&s.v_full[buf], ph, status, abort, 14);
-                ok = ok && mbar_wait_cluster(&s.v_peer[buf], ph, status, abort, 15);
-                if (!ok) return;
-                tc_fence_after();
+            }
+            __syncwarp();
+        };
+        auto issue_pv = [&](uint32_t j, bool first) {
+            const uint32_t buf = j & 1, ph = (j >> 1) & 1;
+            ok = ok && lane0_wait(&s.v_full[buf], ph, 13);
+            ok = ok && lane0_wait(&s.p_full, j & 1, 14);
+            if (!ok) return;
+            if (!leader) {
+                if (lane == 0) mbar_arrive_remote(pv_peer + 8 * buf);
+                return;
+            }
+            ok = lane0_wait_peer(&s.pv_peer[buf], ph, 15);
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
                 const uint64_t vb = vd + buf * (V_STAGE >> 4);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {          // hi, lo
+                for (int c = 0; c < 8; ++c)            // hi, lo
 #pragma unroll
                     for (int h = 0; h < 2; ++h)        // value columns 0-255, 256-511
-                        mma_f8_pair(tmem + TM_O + 128 * h, pd + (c >> 2) * (ATOM >> 4) + (c & 3) * 2,
+                        mma_f8_pair(TM_O + 128 * h, pd + (c >> 2) * (ATOM >> 4) + (c & 3) * 2,
                                     vb + h * (2 * ATOM >> 4) + (c & 3) * (32 * 128 >> 4), c < 4 ? id_ph : id_pl,
                                     c > 0 || !first);
-                }
                 mma_commit_pair(&s.pv_done[buf]);
-            };
-            uint32_t j = 0;
-            if (w.left > 0) issue_s(0, true);
-            while (w.left > 0 && ok) {
-                const int n = w.count();
-                for (int x = 0; x < n && ok; ++x, ++j) {
-                    if (x + 1 < n) issue_s(j + 1, false);
-                    issue_pv(j, x == 0);
-                }
-                w.next(a);
-                if (w.left > 0) issue_s(j, true);
             }
-            mma_commit_pair(&s.drain);
-            mbar_wait_drain(&s.drain, 0, 200000000ull);
-        }
-    } else {
-        // ------------------------------------------------ rank 1: its tiles have landed
-        if (lane == 0) {
-            uint32_t j = 0;
-            bool ok = true;
-            for (long long left = w.left; left > 0 && ok; --left, ++j) {
-                const uint32_t buf = j & 1, ph = (j >> 1) & 1;
-                ok = mbar_wait(&s.k_full[buf], ph, status, abort, 17);
-                if (ok) mbar_arrive_remote(map_to_rank(smem_u32(&s.k_peer[buf]), 0));
-                ok = ok && mbar_wait(&s.v_full[buf], ph, status, abort, 18);
-                if (ok) mbar_arrive_remote(map_to_rank(smem_u32(&s.v_peer[buf]), 0));
+            __syncwarp();
+        };
+        uint32_t j = 0;
+        bool more = __any_sync(0xffffffffu, w.left > 0);
+        if (more) issue_s(0, true);
+        while (more && ok) {
+            const int n = __reduce_max_sync(0xffffffffu, w.count());
+            w.next(a);
+            more = __any_sync(0xffffffffu, w.left > 0);
+            for (int x = 0; x < n && ok; ++x, ++j) {
+                if (x + 1 < n) issue_s(j + 1, false);
+                issue_pv(j, x == 0);
             }
-            mbar_wait_drain(&s.drain, 0, 400000000ull);
+            if (more) issue_s(j, true);
         }
+        if (leader && elect_one()) mma_commit_pair(&s.drain);
+        if (lane == 0) mbar_wait_drain(&s.drain, 0, leader ? 200000000ull : 400000000ull);
     }
     __syncwarp();
     tc_fence_before();
@@ -773,8 +893,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_rows,    // box: 1 row 
 
 // ------------------------------------------------------------------ joining partial results
 // out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the runs that share
-// a unit.  One CTA per 8 rows of a unit, one warp per row; units that one run
-// covered whole have nothing to join.
+// a unit.  A CTA takes 16 of the 32 columns c of each warp's partial result
+// (blockIdx.y = rank, c, half); units that one run covered whole have nothing
+// to join.
 __global__ void __launch_bounds__(256)
 tree_join_kernel(const __grid_constant__ Args a, int max_pairs) {
     __shared__ long long range[3];
@@ -804,34 +925,38 @@ tree_join_kernel(const __grid_constant__ Args a, int max_pairs) {
     const int p0 = pair_with(n, P, begin), p1 = pair_with(n, P, end - 1);
     if (p0 == p1) return;
     const Rows r = unit_rows(a, b, u);
-    const int m = blockIdx.y * 8 + warp;
+    const int rank = blockIdx.y >> 3, c = (blockIdx.y >> 1) & 3, half = blockIdx.y & 1;
+    const int m = rank * HROWS + (warp & 1) * 32 + lane;
     if (m >= r.rows) return;
-    // slot of run p: 0 where it continues the unit, 1 where the unit begins in it
+    // slot of a run: 1 where the unit begins in it, 0 where it continues the unit
+    const int slot0 = 2 * p0 + (run_begin(n, P, p0) > begin ? 0 : 1);
     float top = -INFINITY;
-    for (int p = p0; p <= p1; ++p) {
-        const int slot = 2 * p + (run_begin(n, P, p) > begin ? 0 : 1);
-        top = fmaxf(top, a.part_ml[slot * MROWS + m].x);
-    }
+#pragma unroll 4
+    for (int p = p0; p <= p1; ++p) top = fmaxf(top, a.part_ml[(p == p0 ? slot0 : 2 * p) * MROWS + m].x);
     float4 o[4];
     float l = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int p = p0; p <= p1; ++p) {
-        const int slot = 2 * p + (run_begin(n, P, p) > begin ? 0 : 1);
+        const int slot = p == p0 ? slot0 : 2 * p;
         const float2 ml = a.part_ml[slot * MROWS + m];
+        // a run that saw nothing of the row has weight 0 (its sum is 0, or a NaN that stays)
         const float wgt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_approx(ml.x - top);
-        const float4* po = reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * MROWS + m) * DV) + lane;
         l += wgt * ml.y;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 v = po[32 * i];
-            o[i].x += wgt * v.x; o[i].y += wgt * v.y; o[i].z += wgt * v.z; o[i].w += wgt * v.w;
+            const uint4 v = a.part_o[part_at(slot, rank, warp, c, half * 4 + i, lane)];
+            o[i].x += wgt * __uint_as_float(v.x); o[i].y += wgt * __uint_as_float(v.y);
+            o[i].z += wgt * __uint_as_float(v.z); o[i].w += wgt * __uint_as_float(v.w);
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint2* d = reinterpret_cast<uint2*>(a.out + (r.first + m) * DV) + lane;
+    uint4* d = reinterpret_cast<uint4*>(a.out + (r.first + m) * DV + part_col(warp, c) + 16 * half);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[32 * i] = make_uint2(bf16_pair(o[i].x * inv, o[i].y * inv), bf16_pair(o[i].z * inv, o[i].w * inv));
+    for (int i = 0; i < 2; ++i)
+        d[i] = make_uint4(bf16_pair(o[2 * i].x * inv, o[2 * i].y * inv), bf16_pair(o[2 * i].z * inv, o[2 * i].w * inv),
+                          bf16_pair(o[2 * i + 1].x * inv, o[2 * i + 1].y * inv), bf16_pair(o[2 * i + 1].z * inv, o[2 * i + 1].w * inv));
 }
 
 // ------------------------------------------------------------------ host side
@@ -885,19 +1010,19 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
     const Plan p = plan(pr, k, Hq);
     const int64_t all_units = (int64_t)pr.B * p.units;
     if ((int64_t)pr.B * pr.Lq > 0x7fffffffLL || all_units > 0x7fffffffLL) return IC_ERR_UNSUPPORTED;
-    CUtensorMap map_rows, map_box;
-    const int64_t rows = (int64_t)pr.num_pages * pr.page_size;
-    if (!make_map(&map_rows, kv_q8, rows, 1) || !make_map(&map_box, kv_q8, rows, 64)) return cuda_error("tree_attn_q8");
+    CUtensorMap map_box;
+    if (!make_map(&map_box, kv_q8, (int64_t)pr.num_pages * pr.page_size, 64)) return cuda_error("tree_attn_q8");
     Args a;
     a.q = static_cast<const __nv_bfloat16*>(q);
+    a.cache = static_cast<const uint8_t*>(kv_q8);
     a.kv_scale = kv_scale;
     a.idx = idx;
     a.tree = reinterpret_cast<const unsigned long long*>(tree);
     a.seq_lens = pr.seq_lens;
     a.block_table = pr.block_table;
     a.out = static_cast<__nv_bfloat16*>(out);
-    a.part_o = static_cast<float*>(scratch);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)p.pairs * 2 * MROWS * DV);
+    a.part_o = static_cast<uint4*>(scratch);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)p.pairs * 2 * PART);
     a.status = status;
     a.k = k;
     a.B = pr.B;
@@ -913,15 +1038,14 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
     if (cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES) != cudaSuccess)
         return cuda_error("tree_attn_q8");
     const bool pdl = pdl_rows((int64_t)pr.B * pr.Lq);
-    if (launch_ex(tree_attn_kernel, dim3((unsigned)(2 * p.pairs)), dim3(THREADS), SMEM_BYTES, s, pdl, 0, map_rows, map_box,
-                  a) != cudaSuccess)
+    if (launch_ex(tree_attn_kernel, dim3((unsigned)(2 * p.pairs)), dim3(THREADS), SMEM_BYTES, s, pdl, 0, map_box, a) != cudaSuccess)
         return cuda_error("tree_attn_q8");
     count_launch(IC_LK_TREE);
     ic_status st = last_launch_status();
     // with lists the host knows the runs: every unit may be whole
     const bool joins = !k || p.blocks % p.pairs != 0 || (p.blocks / p.pairs) % p.list_blocks != 0;
     if (st != IC_OK || !joins) return st;
-    if (launch_ex(tree_join_kernel, dim3((unsigned)all_units, MROWS / 8), dim3(256), 0, s, pdl, 0, a, p.pairs) != cudaSuccess)
+    if (launch_ex(tree_join_kernel, dim3((unsigned)all_units, 16), dim3(256), 0, s, pdl, 0, a, p.pairs) != cudaSuccess)
         return cuda_error("tree_join");
     count_launch(IC_LK_COMBINE);
     return last_launch_status();

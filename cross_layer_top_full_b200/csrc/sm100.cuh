@@ -372,12 +372,6 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     }
 }
 
-// Remote arrive that publishes this thread's earlier writes to the cluster.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-                 : "memory");
-}
-
 // Orders this thread's shared-memory writes before later reads of the async
 // proxy (TMA, tcgen05.mma).
 __device__ __forceinline__ void fence_async_smem() {

@@ -268,9 +268,11 @@ __device__ __forceinline__ uint32_t tree_bits(unsigned long long mask, int off) 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {   // the rest of 16: zeros
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// This thread's arrival at `bar` once its copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // A partial result of a unit: O of one thread (row (warp & 1) * 32 + lane of
 // CTA rank) in 16-byte pieces i = 0..7 of 32 columns c = 0..3 from
@@ -302,7 +304,6 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int row0, const uint8_t*
         for (int c = 0; c < ATOMS; ++c)
             copy16((g & 1 ? d1 : d0) + (g >> 1) * 1024 + c * DST, src + c * STEP, bytes);
     }
-    copy_commit();
 }
 
 // ------------------------------------------------------------------ Q of a unit
@@ -409,8 +410,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             mbar_init(&s.info_free[i], SOFT_WARPS + 4);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.k_full[i], 2);
-            mbar_init(&s.v_full[i], 2);
+            mbar_init(&s.k_full[i], 64);
+            mbar_init(&s.v_full[i], 64);
             mbar_init(&s.s_peer[i], 1);
             mbar_init(&s.pv_peer[i], 1);
             mbar_init(&s.s_full[i], 1);
@@ -572,14 +573,15 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 if (j > 0) warp_wait(&s.pv_done[buf ^ 1], ((j - 1) >> 1) & 1, status, abort, 7);
                 if (x > 0 && __any_sync(0xffffffffu, grow)) {
                     tc_fence_after();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t addr = tmem + lane_base + TM_O + 128 * grp + 32 * c;
-                        tmem_ld32(addr, t);
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {
+                        const uint32_t addr = tmem + lane_base + TM_O + 128 * grp + 16 * c;
+                        uint32_t o[16];
+                        tmem_ld16(addr, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) t[i] = __float_as_uint(__uint_as_float(t[i]) * factor);
-                        tmem_st32(addr, t);
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+                        tmem_st16(addr, o);
                     }
                     tmem_st_wait();
                 }
@@ -663,9 +665,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
     } else if (warp < W_RES) {
         // ------------------------------------------------ copies of the tiles
         // K: this CTA's 64 keys whole, 32 rows per warp; V: its columns of all
-        // keys, 64 rows per warp.  A block's copies are waited for after the
-        // next block's are sent: K(j + 1) is sent when S(j - 1) is complete,
-        // which is before S(j) can begin, and V alike.
+        // keys, 64 rows per warp.  Every lane's arrival comes with its copies;
+        // who waits for a tile orders them before its MMAs (fence_async_smem).
         const bool is_k = warp < W_COPY + 2;
         const int mine = (warp - W_COPY) & 1;
         const int stage_bytes = is_k ? K_STAGE : V_STAGE;
@@ -673,7 +674,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
         uint64_t* full = is_k ? s.k_full : s.v_full;
         uint64_t* freed = is_k ? s.s_full : s.pv_done;
         uint32_t j = 0, slot = 0, turn = 0;
-        bool ok = true, pending = false;
+        bool ok = true;
         for (long long left = w.left; left > 0; --left, ++j) {
             const uint32_t buf = j & 1;
             ok = warp_wait(&s.info_full[slot], turn & 1, status, abort, 1);
@@ -693,31 +694,19 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                         for (int c = 0; c < 4; ++c)
                             tma_load_2d(d + c * ATOM, &map_box, &full[buf], (c >> 1) * 256 + (int)rank * 128,
                                         info.rows[0] + (c & 1) * 64);
-                } else if (lane == 0) {
+                } else {
                     mbar_arrive(&full[buf]);
                 }
             } else {
                 if (is_k) copy_rows<8, 5, 128, ATOM>(dst0, mine * 32, a.cache, info.rows + (int)rank * HROWS + mine * 32, lane);
                 else copy_rows<16, 2, 256, 2 * ATOM>(dst0, mine * 64, a.cache + rank * 128, info.rows + mine * 64, lane);
+                copy_arrive(&full[buf]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.info_free[slot]);
             if (++slot == RING) { slot = 0; ++turn; }
-            if (pending) {
-                if (box) copy_wait<0>();
-                else copy_wait<1>();
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[buf ^ 1]);
-            }
-            pending = !box;
         }
-        copy_wait<0>();
-        if (pending && ok) {
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[(j - 1) & 1]);
-        }
+        copy_wait_all();
         // boxes have landed before the CTA exits, whatever happened
         for (uint32_t i = j > 2 ? j - 2 : 0; i < j; ++i) mbar_wait_drain(&full[i & 1], (i >> 1) & 1, 200000000ull);
     } else if (warp < W_MMA) {
@@ -792,7 +781,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
     } else if (warp == W_MMA) {
         // ------------------------------------------------ MMA issue; rank 1 passes its readiness on
         // (counts and outcomes of waits go through votes, which keeps the
-        // control flow uniform)
+        // control flow uniform).  What rank 1 passes on never leaves its SM,
+        // whose tensor core reads it there, and its own waits and fence come
+        // first: the arrival itself needs no release at cluster scope, which
+        // took 2000 cycles a block here.
         constexpr uint32_t id_s = idesc_f32acc(0, 0, MROWS, NB), id_r = idesc_f32acc(1, 1, MROWS, NB);
         constexpr uint32_t id_ph = idesc_f32acc(0, 0, MROWS, 256, 0, 1), id_pl = idesc_f32acc(1, 0, MROWS, 256, 0, 1);
         const uint64_t qd = desc_sw128(sbase + OFF_Q, 16, 1024), kd = desc_sw128(sbase + OFF_K, 16, 1024);
@@ -816,8 +808,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             if (first) ok = ok && lane0_wait(&s.q_full, unit++ & 1, 10);
             ok = ok && lane0_wait(&s.k_full[buf], ph, 11);
             if (!ok) return;
+            fence_async_smem();
             if (!leader) {
-                if (lane == 0) mbar_arrive_remote(s_peer + 8 * buf);
+                if (lane == 0) mbar_arrive_remote_relaxed(s_peer + 8 * buf);
                 return;
             }
             ok = lane0_wait_peer(&s.s_peer[buf], ph, 12);
@@ -845,8 +838,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             ok = ok && lane0_wait(&s.v_full[buf], ph, 13);
             ok = ok && lane0_wait(&s.p_full, j & 1, 14);
             if (!ok) return;
+            fence_async_smem();
             if (!leader) {
-                if (lane == 0) mbar_arrive_remote(pv_peer + 8 * buf);
+                if (lane == 0) mbar_arrive_remote_relaxed(pv_peer + 8 * buf);
                 return;
             }
             ok = lane0_wait_peer(&s.pv_peer[buf], ph, 15);

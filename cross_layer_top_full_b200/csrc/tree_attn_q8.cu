@@ -73,7 +73,7 @@ constexpr int OFF_P = OFF_V + 2 * V_STAGE;
 constexpr int RING = 3;
 struct Info {                                 // one block, resolved
     int rows[NB];                             // cache rows, -1: seen by nobody
-    uint32_t scale[NB];                       // bfloat16 pairs: log2 of the scale, the scale above it
+    float scale[NB], lg[NB], inv[NB];         // scales, their log2 and inverse
     uint32_t seen[NB / 32];                   // bit: not -1
     int box;                                  // 128 consecutive cache rows from rows[0] on
     int pad[3];
@@ -108,9 +108,7 @@ struct __align__(8) Bars {
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
-    int start_b, start_u, start_t;
-    int pad;
-    long long left;
+    int start_b, start_u, start_t, left;
 };
 constexpr size_t SMEM_BYTES = 1008 + OFF_BARS + sizeof(Bars);
 static_assert(SMEM_BYTES <= 232448 && OFF_BARS % 8 == 0, "shared memory budget");
@@ -142,29 +140,30 @@ __device__ __forceinline__ int blocks_of(const Args& a, int b) {
     return a.idx ? a.list_blocks : max(1, (seq_len(a, b) + NB - 1) / NB);
 }
 
-// All blocks of the call (one warp).
-__device__ __forceinline__ long long total_blocks(const Args& a) {
-    if (a.idx) return (long long)a.B * a.units * a.list_blocks;
-    long long n = 0;
+// All blocks of the call (one warp); the host has made sure that they fit.
+__device__ __forceinline__ int total_blocks(const Args& a) {
+    if (a.idx) return a.B * a.units * a.list_blocks;
+    int n = 0;
     for (int b = threadIdx.x & 31; b < a.B; b += 32) n += blocks_of(a, b);
-    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n * a.units;
+    return __reduce_add_sync(0xffffffffu, n) * a.units;
 }
 
-// Runs of the pairs: pair p of P takes blocks [p n / P, (p+1) n / P).
-__device__ __forceinline__ int pairs_of(long long n, int max_pairs) { return n < max_pairs ? (int)n : max_pairs; }
-__device__ __forceinline__ long long run_begin(long long n, int P, int p) { return n * p / P; }
-__device__ __forceinline__ int pair_with(long long n, int P, long long t) { return (int)(((t + 1) * P - 1) / n); }
+// Runs of the pairs: n blocks over P pairs, the first n % P one block longer.
+__device__ __forceinline__ int pairs_of(int n, int max_pairs) { return min(n, max_pairs); }
+__device__ __forceinline__ int run_begin(int n, int P, int p) { return n / P * p + min(n % P, p); }
+__device__ __forceinline__ int pair_with(int n, int P, int t) {
+    const int q = n / P, longer = n % P, at = longer * (q + 1);
+    return t < at ? t / (q + 1) : longer + (t - at) / q;
+}
 
 // A walk over a run: unit u of sequence b, from block t on.
 struct Walk {
-    int b, u, t, nt;
-    long long left;
+    int b, u, t, nt, left;
     __device__ __forceinline__ void start(const Args& a, const Bars& s) {
         b = s.start_b; u = s.start_u; t = s.start_t; left = s.left;
         nt = left > 0 ? blocks_of(a, b) : 0;
     }
-    __device__ __forceinline__ int count() const { return left < nt - t ? (int)left : nt - t; }
+    __device__ __forceinline__ int count() const { return min(left, nt - t); }
     __device__ __forceinline__ void next(const Args& a) {
         left -= count();
         t = 0;
@@ -225,9 +224,6 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-
-// 2^-n of a packed scale 2^n (its bfloat16 in the upper half).
-__device__ __forceinline__ float inverse_of(uint32_t packed) { return __uint_as_float(0x7f000000u - (packed & 0xffff0000u)); }
 
 // Two e4m3 numbers and two e5m2 numbers for what they leave of (a, b).
 __device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
@@ -424,25 +420,22 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
     if (warp == W_MMA) tmem_alloc_pair<TMEM_COLS>(&s.tmem_base);
     pdl_wait();
     if (warp == W_RES) {             // this pair's run
-        const long long n = total_blocks(a);
-        const int P = pairs_of(n, gridDim.x / 2), p = blockIdx.x / 2;
-        long long begin = 0, left = 0;
+        const int n = total_blocks(a), P = pairs_of(n, gridDim.x / 2), p = blockIdx.x / 2;
+        int begin = 0, left = 0;
         if (p < P) {
             begin = run_begin(n, P, p);
             left = run_begin(n, P, p + 1) - begin;
         }
-        int b = 0;
-        long long off = begin;       // blocks between sequence b's first and the run's first
+        int b = 0, off = begin;      // off: blocks between sequence b's first and the run's first
         if (a.idx) {
-            const long long per = (long long)a.units * a.list_blocks;
-            b = (int)(begin / per);
-            off = begin % per;
+            b = begin / (a.units * a.list_blocks);
+            off = begin % (a.units * a.list_blocks);
         } else if (left > 0) {
             for (int b0 = 0; b0 < a.B; b0 += 32) {
-                const long long c = b0 + lane < a.B ? (long long)blocks_of(a, b0 + lane) * a.units : 0;
-                long long x = c;     // inclusive prefix sum
+                const int c = b0 + lane < a.B ? blocks_of(a, b0 + lane) * a.units : 0;
+                int x = c;           // inclusive prefix sum
                 for (int o = 1; o < 32; o <<= 1) {
-                    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
                     if (lane >= o) x += y;
                 }
                 const unsigned hit = __ballot_sync(0xffffffffu, off < x);
@@ -458,8 +451,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
         if (lane == 0) {
             const int nt = left > 0 ? blocks_of(a, b) : 1;
             s.start_b = b;
-            s.start_u = (int)(off / nt);
-            s.start_t = (int)(off % nt);
+            s.start_u = off / nt;
+            s.start_t = off % nt;
             s.left = left;
         }
     }
@@ -488,14 +481,61 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
         uint32_t j = 0, slot = 0, turn = 0;         // block j is use `turn` of ring slot `slot`
         Rows r{};
         float sq = 0.f;
-        if (w.left > 0) {
-            r = unit_rows(a, w.b, w.u);
-            sq = convert_q(a, r, smem, s, rank, tmem, lane_base, 0);
-        }
-        while (w.left > 0) {
+        const int m = (int)rank * HROWS + row;      // query row of a unit
+        Rows done{};
+        float mref = -INFINITY, l = 0.f;
+        bool whole = false;
+        int part_slot = 0;
+        while (true) {
+            // this unit's Q, then the results of the unit before
+            if (w.left > 0) {
+                r = unit_rows(a, w.b, w.u);
+                sq = convert_q(a, r, smem, s, rank, tmem, lane_base, j);
+            }
+            if (j > 0) {
+                xl[part * HROWS + row] = l;
+                soft_sync();
+                l = (xl[row] + xl[HROWS + row]) + (xl[2 * HROWS + row] + xl[3 * HROWS + row]);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const bool ok = warp_wait(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, status, abort, 9);
+                tc_fence_after();
+                uint8_t* stage = smem + OFF_P + warp * 2048;       // 32 rows x 64 bytes
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t t[32];
+                    tmem_ld32(tmem + lane_base + TM_O + 128 * grp + 32 * c, t);
+                    tmem_ld_wait();
+                    if (whole) {
+                        // through shared memory, so that four lanes write 64 adjacent bytes of a row
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                u[k] = bf16_pair(__uint_as_float(t[8 * i + 2 * k]) * inv, __uint_as_float(t[8 * i + 2 * k + 1]) * inv);
+                            *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int rr = 8 * i + (lane >> 2), mm = (int)rank * HROWS + (warp & 1) * 32 + rr;
+                            const uint4 o = *reinterpret_cast<const uint4*>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+                            if (ok && mm < done.rows)
+                                *(reinterpret_cast<uint4*>(a.out + (done.first + mm) * DV + part_col(warp, c)) + (lane & 3)) = o;
+                        }
+                        __syncwarp();
+                    } else if (ok) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            a.part_o[part_at(part_slot, rank, warp, c, i, lane)] = make_uint4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
+                    }
+                }
+                if (!whole && ok && part == 0) a.part_ml[part_slot * MROWS + m] = make_float2(mref, l);
+                tc_fence_before();
+            }
+            if (w.left <= 0) break;
             const int n = w.count(), len = seq_len(a, w.b), ctx = len - a.Lq;
             const bool dense = a.idx == nullptr;
-            const int m = (int)rank * HROWS + row;          // of the unit
             unsigned long long mask = ~0ull;                // nodes that this row sees
             if (dense && m < r.rows) {
                 const int i = (r.node0 + m) / a.Hq;
@@ -503,7 +543,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             }
             const float arow = sq * a.scale_log2;
             const uint64_t a2 = f2(arow, arow);
-            float mref = -INFINITY, l = 0.f;
+            mref = -INFINITY;
+            l = 0.f;
             for (int x = 0; x < n; ++x, ++j) {
                 const uint32_t buf = j & 1, ph = (j >> 1) & 1;
                 const int s0 = (w.t + x) * NB;              // the block's first entry
@@ -513,33 +554,29 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 tc_fence_after();
                 uint32_t t[32];
                 tmem_ld32(tmem + lane_base + TM_S + 64 * buf + 32 * grp, t);
-                const uint4* g4 = reinterpret_cast<const uint4*>(info.scale) + kw * 8;
+                const float4* g4 = reinterpret_cast<const float4*>(info.scale) + kw * 8;
                 uint32_t seen = info.seen[kw];
                 if (dense) seen &= tree_bits(mask, s0 + kw * 32 - ctx);
-                uint32_t g[32];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint4 x = g4[c];
-                    g[4 * c] = x.x; g[4 * c + 1] = x.y; g[4 * c + 2] = x.z; g[4 * c + 3] = x.w;
-                }
                 tmem_ld_wait();
                 float y[32];
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                    const float2 u = f2_split(ffma2(fmul2(f2(__uint_as_float(t[c]), __uint_as_float(t[c + 1])), a2),
-                                                    f2(__uint_as_float(g[c] & 0xffff0000u), __uint_as_float(g[c + 1] & 0xffff0000u)),
-                                                    f2(__uint_as_float(g[c] << 16), __uint_as_float(g[c + 1] << 16))));
-                    y[c] = u.x;
-                    y[c + 1] = u.y;
+                for (int c = 0; c < 8; ++c) {
+                    const float4 g = g4[c], lg = g4[NB / 4 + c];
+                    const float2 u = f2_split(ffma2(fmul2(f2(__uint_as_float(t[4 * c]), __uint_as_float(t[4 * c + 1])), a2),
+                                                    f2(g.x, g.y), f2(lg.x, lg.y)));
+                    const float2 v = f2_split(ffma2(fmul2(f2(__uint_as_float(t[4 * c + 2]), __uint_as_float(t[4 * c + 3])), a2),
+                                                    f2(g.z, g.w), f2(lg.z, lg.w)));
+                    y[4 * c] = u.x; y[4 * c + 1] = u.y; y[4 * c + 2] = v.x; y[4 * c + 3] = v.y;
                 }
                 if (seen != 0xffffffffu) {
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
                         if (!((seen >> c) & 1u)) y[c] = -INFINITY;
                 }
-                float mx = fmaxf(y[0], y[1]);
+                float mx = -INFINITY;
 #pragma unroll
-                for (int c = 2; c < 32; c += 2) mx = fmaxf(mx, fmaxf(y[c], y[c + 1]));
+                for (int c = 0; c < 8; ++c)
+                    mx = fmaxf(mx, fmaxf(fmaxf(y[c], y[c + 8]), fmaxf(y[c + 16], y[c + 24])));
                 float* xm = reinterpret_cast<float*>(smem + OFF_XM) + buf * (4 * HROWS);
                 xm[part * HROWS + row] = mx;
                 soft_sync();
@@ -556,8 +593,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                     const float2 u = f2_split(fadd2(f2(y[c], y[c + 1]), off2));
                     const float2 v = f2_split(fadd2(f2(y[c + 2], y[c + 3]), off2));
                     const float e0 = ex2_approx(u.x), e1 = ex2_approx(u.y), e2 = ex2_approx(v.x), e3 = ex2_approx(v.y);
-                    l2 = ffma2(f2(e0, e1), f2(inverse_of(g[c]), inverse_of(g[c + 1])), l2);
-                    l2 = ffma2(f2(e2, e3), f2(inverse_of(g[c + 2]), inverse_of(g[c + 3])), l2);
+                    const float4 inv = g4[2 * (NB / 4) + c / 4];
+                    l2 = ffma2(f2(e0, e1), f2(inv.x, inv.y), l2);
+                    l2 = ffma2(f2(e2, e3), f2(inv.z, inv.w), l2);
                     uint32_t h0, h1, r0, r1;
                     split_weights(e0, e1, h0, r0);
                     split_weights(e2, e3, h1, r1);
@@ -598,6 +636,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                     // NaN by themselves.
                     warp_wait(&s.v_full[buf], ph, status, abort, 8);
                     uint4* v = reinterpret_cast<uint4*>(smem + OFF_V + buf * V_STAGE) + threadIdx.x;
+#pragma unroll 1
                     for (int c = 0; c < V_STAGE / 16 / 256; ++c) {
                         const uint4 o = v[c * 256];
                         uint4 z = o;
@@ -613,54 +652,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.p_full);
             }
-            // the next unit's Q, then this unit's results
-            const Rows done = r;
-            const bool whole = w.t == 0 && n == w.nt;
-            const int part_slot = (blockIdx.x / 2) * 2 + (w.t > 0 ? 0 : 1);
+            done = r;
+            whole = w.t == 0 && n == w.nt;
+            part_slot = (blockIdx.x / 2) * 2 + (w.t > 0 ? 0 : 1);
             w.next(a);
-            if (w.left > 0) {
-                r = unit_rows(a, w.b, w.u);
-                sq = convert_q(a, r, smem, s, rank, tmem, lane_base, j);
-            }
-            xl[part * HROWS + row] = l;
-            soft_sync();
-            l = (xl[row] + xl[HROWS + row]) + (xl[2 * HROWS + row] + xl[3 * HROWS + row]);
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const bool ok = warp_wait(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, status, abort, 9);
-            tc_fence_after();
-            uint8_t* stage = smem + OFF_P + warp * 2048;       // 32 rows x 64 bytes
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t t[32];
-                tmem_ld32(tmem + lane_base + TM_O + 128 * grp + 32 * c, t);
-                tmem_ld_wait();
-                if (whole) {
-                    // through shared memory, so that four lanes write 64 adjacent bytes of a row
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t u[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            u[k] = bf16_pair(__uint_as_float(t[8 * i + 2 * k]) * inv, __uint_as_float(t[8 * i + 2 * k + 1]) * inv);
-                        *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int rr = 8 * i + (lane >> 2), mm = (int)rank * HROWS + (warp & 1) * 32 + rr;
-                        const uint4 o = *reinterpret_cast<const uint4*>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-                        if (ok && mm < done.rows)
-                            *(reinterpret_cast<uint4*>(a.out + (done.first + mm) * DV + part_col(warp, c)) + (lane & 3)) = o;
-                    }
-                    __syncwarp();
-                } else if (ok) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        a.part_o[part_at(part_slot, rank, warp, c, i, lane)] = make_uint4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
-                }
-            }
-            if (!whole && ok && part == 0) a.part_ml[part_slot * MROWS + m] = make_float2(mref, l);
-            tc_fence_before();
         }
     } else if (warp < W_RES) {
         // ------------------------------------------------ copies of the tiles
@@ -675,7 +670,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
         uint64_t* freed = is_k ? s.s_full : s.pv_done;
         uint32_t j = 0, slot = 0, turn = 0;
         bool ok = true;
-        for (long long left = w.left; left > 0; --left, ++j) {
+        for (int left = w.left; left > 0; --left, ++j) {
             const uint32_t buf = j & 1;
             ok = warp_wait(&s.info_full[slot], turn & 1, status, abort, 1);
             if (ok && j >= 2) ok = warp_wait(&freed[buf], ((j - 2) >> 1) & 1, status, abort, is_k ? 2 : 3);
@@ -742,14 +737,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 }
                 int page[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) page[i] = rows[i] >= 0 ? __ldg(table + rows[i] / a.page_size) : -1;
+                for (int i = 0; i < 4; ++i) {
+                    const int at = max(rows[i], 0) / a.page_size;
+                    page[i] = rows[i] >= 0 ? __ldg(table + at) : -1;
+                    rows[i] -= at * a.page_size;       // its place in the page (negative: seen by nobody)
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (rows[i] >= 0 && (page[i] < 0 || page[i] >= a.num_pages)) {
                         flag_status(status, IC_DEV_INDEX_RANGE);
                         page[i] = -1;
                     }
-                    rows[i] = page[i] >= 0 ? page[i] * a.page_size + rows[i] % a.page_size : -1;
+                    rows[i] = page[i] >= 0 ? page[i] * a.page_size + rows[i] : -1;
                     valid |= page[i] >= 0 ? 1u << i : 0u;
                 }
 #pragma unroll
@@ -759,18 +758,22 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 word |= __shfl_xor_sync(0xffffffffu, word, 1);
                 word |= __shfl_xor_sync(0xffffffffu, word, 2);
                 word |= __shfl_xor_sync(0xffffffffu, word, 4);
-                uint32_t packed[4];
+                float lg[4], inv[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t u = __float_as_uint(g[i]) & 0x7f800000u;      // a power of two
-                    packed[i] = u | __float_as_uint((float)((int)(u >> 23) - 127)) >> 16;
+                for (int i = 0; i < 4; ++i) {          // a power of two
+                    const uint32_t u = __float_as_uint(g[i]) & 0x7f800000u;
+                    g[i] = __uint_as_float(u);
+                    lg[i] = (float)((int)(u >> 23) - 127);
+                    inv[i] = __uint_as_float(0x7f000000u - u);
                 }
                 const uint32_t slot = j % RING, turn = j / RING;
                 if (turn > 0) ok = warp_wait(&s.info_free[slot], (turn - 1) & 1, status, abort, 16);
                 if (!ok) break;
                 Info& info = reinterpret_cast<Info*>(smem + OFF_INFO)[slot];
                 reinterpret_cast<int4*>(info.rows)[lane] = make_int4(rows[0], rows[1], rows[2], rows[3]);
-                reinterpret_cast<uint4*>(info.scale)[lane] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+                reinterpret_cast<float4*>(info.scale)[lane] = make_float4(g[0], g[1], g[2], g[3]);
+                reinterpret_cast<float4*>(info.lg)[lane] = make_float4(lg[0], lg[1], lg[2], lg[3]);
+                reinterpret_cast<float4*>(info.inv)[lane] = make_float4(inv[0], inv[1], inv[2], inv[3]);
                 if ((lane & 7) == 0) info.seen[lane >> 3] = word;
                 if (lane == 0) info.box = box;
                 __syncwarp();
@@ -848,7 +851,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             tc_fence_after();
             if (elect_one()) {
                 const uint64_t vb = vd + buf * (V_STAGE >> 4);
-#pragma unroll
+#pragma unroll 4
                 for (int c = 0; c < 8; ++c)            // hi, lo
 #pragma unroll
                     for (int h = 0; h < 2; ++h)        // value columns 0-255, 256-511
@@ -859,18 +862,23 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             }
             __syncwarp();
         };
-        uint32_t j = 0;
-        bool more = __any_sync(0xffffffffu, w.left > 0);
-        if (more) issue_s(0, true);
-        while (more && ok) {
-            const int n = __reduce_max_sync(0xffffffffu, w.count());
-            w.next(a);
-            more = __any_sync(0xffffffffu, w.left > 0);
-            for (int x = 0; x < n && ok; ++x, ++j) {
-                if (x + 1 < n) issue_s(j + 1, false);
-                issue_pv(j, x == 0);
+        // S(j + 1) goes before P V(j) inside a unit and after it where a new
+        // unit begins (its Q is not ready earlier)
+        int js = 0, jp = 0, unit_begin = 0, unit_end = 0;      // next S, next P V; the latter's unit
+        const int total = __reduce_max_sync(0xffffffffu, w.left);
+        while (ok && jp < total) {
+            if (jp == unit_end) {
+                unit_begin = unit_end;
+                unit_end += __reduce_max_sync(0xffffffffu, w.count());
+                w.next(a);
             }
-            if (more) issue_s(j, true);
+            if (js < unit_end && js <= jp + 1) {
+                issue_s(js, js == unit_begin);
+                ++js;
+            } else {
+                issue_pv(jp, jp == unit_begin);
+                ++jp;
+            }
         }
         if (leader && elect_one()) mma_commit_pair(&s.drain);
         if (lane == 0) mbar_wait_drain(&s.drain, 0, leader ? 200000000ull : 400000000ull);
@@ -892,20 +900,19 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
 // to join.
 __global__ void __launch_bounds__(256)
 tree_join_kernel(const __grid_constant__ Args a, int max_pairs) {
-    __shared__ long long range[3];
+    __shared__ int range[3];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.x / a.units, u = blockIdx.x % a.units;
     pdl_trigger();
     pdl_wait();
     if (warp == 0) {
-        const long long n = total_blocks(a);
-        long long begin = 0;
+        const int n = total_blocks(a);
+        int begin = 0;
         if (a.idx) {
-            begin = (long long)blockIdx.x * a.list_blocks;
+            begin = blockIdx.x * a.list_blocks;
         } else {
             for (int i = lane; i < b; i += 32) begin += blocks_of(a, i);
-            for (int o = 16; o; o >>= 1) begin += __shfl_xor_sync(0xffffffffu, begin, o);
-            begin = begin * a.units + (long long)u * blocks_of(a, b);
+            begin = __reduce_add_sync(0xffffffffu, begin) * a.units + u * blocks_of(a, b);
         }
         if (lane == 0) {
             range[0] = n;
@@ -914,7 +921,7 @@ tree_join_kernel(const __grid_constant__ Args a, int max_pairs) {
         }
     }
     __syncthreads();
-    const long long n = range[0], begin = range[1], end = range[2];
+    const int n = range[0], begin = range[1], end = range[2];
     const int P = pairs_of(n, max_pairs);
     const int p0 = pair_with(n, P, begin), p1 = pair_with(n, P, end - 1);
     if (p0 == p1) return;
@@ -931,7 +938,7 @@ tree_join_kernel(const __grid_constant__ Args a, int max_pairs) {
     float l = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 2
     for (int p = p0; p <= p1; ++p) {
         const int slot = p == p0 ? slot0 : 2 * p;
         const float2 ml = a.part_ml[slot * MROWS + m];
@@ -1003,7 +1010,7 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
                               void* out, uint32_t* status, void* scratch, cudaStream_t s) {
     const Plan p = plan(pr, k, Hq);
     const int64_t all_units = (int64_t)pr.B * p.units;
-    if ((int64_t)pr.B * pr.Lq > 0x7fffffffLL || all_units > 0x7fffffffLL) return IC_ERR_UNSUPPORTED;
+    if ((int64_t)pr.B * pr.Lq > 0x7fffffffLL || p.blocks > 0x7fffffffLL) return IC_ERR_UNSUPPORTED;
     CUtensorMap map_box;
     if (!make_map(&map_box, kv_q8, (int64_t)pr.num_pages * pr.page_size, 64)) return cuda_error("tree_attn_q8");
     Args a;

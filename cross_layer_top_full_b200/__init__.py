@@ -429,65 +429,80 @@ def layer_stack_forward_paged(pattern: str, layers: Sequence[Dict], shape: Stack
 
 
 # --------------------------------------------------------------------------- quantised cache
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+def _refuse(x, name: str, dtypes, shape, device: int) -> None:
+    """Says what is wrong with a tensor that a check below turned down."""
+    if x.get_device() != device:
+        raise ValueError("%s: expected a tensor on cuda:%d, the current device, got %s" % (name, device, x.device))
+    if x.dtype not in dtypes:
+        raise ValueError("%s: unexpected dtype %s" % (name, x.dtype))
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(x.shape)))
+    raise ValueError("%s: expected a contiguous tensor (caches, lists) or rows of adjacent values, got strides %s"
+                     % (name, tuple(x.stride())))
 
 
-def _shaped(x, name: str, dtypes, shape, device, strided: bool = False):
-    """Address of a CUDA tensor on `device` (the current device) of one of
-    `dtypes` whose shape matches (None: any size); contiguous, or with
-    `strided` a 2-D tensor whose rows may lie apart."""
-    _need(x.is_cuda and x.device.index == device,
-          "%s: expected a tensor on cuda:%s, the current device, got %s" % (name, device, x.device))
-    _need(x.dtype in dtypes, "%s: unexpected dtype %s" % (name, x.dtype))
-    _need(x.dim() == len(shape) and all(want is None or have == want
-                                        for have, want in zip(x.shape, shape)),
-          "%s: expected shape %s, got %s" % (name, shape, tuple(x.shape)))
-    if strided:
-        _need(x.shape[0] <= 1 or (x.stride(1) == 1 and x.stride(0) >= x.shape[1]),
-              "%s: expected rows of adjacent values, got strides %s" % (name, x.stride()))
-        _need(x.shape[0] != 1 or x.stride(1) == 1,
-              "%s: expected rows of adjacent values, got strides %s" % (name, x.stride()))
-    else:
-        _need(x.is_contiguous(), "%s: expected a contiguous tensor, got strides %s" % (name, x.stride()))
+# These calls are short (a few microseconds on the device), so each check is
+# one comparison and the reasons are worked out only on the way to an error.
+def _dense(x, name: str, dtypes, shape, device: int) -> int:
+    """Address of a contiguous CUDA tensor of the given shape."""
+    if x.get_device() != device or x.dtype not in dtypes or x.shape != shape or not x.is_contiguous():
+        _refuse(x, name, dtypes, shape, device)
     return x.data_ptr()
 
 
-def _row_stride(x) -> int:
-    return max(x.stride(0), x.shape[1])      # one row or none: its stride means nothing
+def _rows_of(x, name: str, dtypes, width: int, n: int, device: int):
+    """Address and row stride of n rows of adjacent values that may lie apart."""
+    if x.get_device() != device or x.dtype not in dtypes or x.shape != (n, width):
+        _refuse(x, name, dtypes, (n, width), device)
+    if n == 0:
+        return x.data_ptr(), width
+    step, unit = x.stride()
+    if unit != 1 or (step < width and n > 1):
+        _refuse(x, name, dtypes, (n, width), device)
+    return x.data_ptr(), step if n > 1 else width        # one row: its stride means nothing
 
 
-def _q8_rows(where, slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale, stream):
-    """The checked arguments that writing and reading share."""
+def _workspace(ws, device: int):
+    import torch
+    n = ws.shape[0] if ws.dim() == 1 else -1
+    return _dense(ws, "ws", (torch.uint8,), (n,), device), n
+
+
+def _current(device: int, stream) -> Optional[int]:
+    if stream is not None:
+        return _stream(stream)
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _q8_rows(where, slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale):
+    """The checked arguments that writing and reading share: rows and caches
+    (address, stride), type, counts, workspace."""
     import torch
     device = torch.cuda.current_device()
-    latent, index = kv is not None, k_idx is not None
-    _need(latent or index, "%s: give kv, k_idx or both" % where)
-    _need(latent == (kv_q8 is not None) == (kv_scale is not None) if latent else
-          kv_q8 is None and kv_scale is None, "%s: kv, kv_q8 and kv_scale go together" % where)
-    _need(index == (k_codes is not None) == (k_scale is not None) if index else
-          k_codes is None and k_scale is None, "%s: k_idx, k_codes and k_scale go together" % where)
-    rows = kv if latent else k_idx
-    n, num_rows = rows.shape[0], (kv_q8 if latent else k_codes).shape[0]
-    dtypes = (rows.dtype,) if rows.dtype in (torch.bfloat16, torch.float32) else ()
-    u8 = (torch.uint8, torch.float8_e4m3fn)
-    a = dict(kv=None, kvs=576, kq=None, ks=None, ki=None, kis=128, kc=None, ksc=None)
-    if latent:
-        a["kv"] = _shaped(kv, "kv", dtypes, (n, 576), device, strided=True)
-        a["kvs"] = _row_stride(kv)
-        a["kq"] = _shaped(kv_q8, "kv_q8", (torch.uint8,), (num_rows, Q8_ROW_BYTES), device)
-        a["ks"] = _shaped(kv_scale, "kv_scale", (torch.float32,), (num_rows,), device)
-    if index:
-        a["ki"] = _shaped(k_idx, "k_idx", dtypes, (n, 128), device, strided=True)
-        a["kis"] = _row_stride(k_idx)
-        a["kc"] = _shaped(k_codes, "k_codes", u8, (num_rows, 128), device)
-        a["ksc"] = _shaped(k_scale, "k_scale", (torch.float32,), (num_rows,), device)
-    a["slots"] = None if slots is None else _shaped(slots, "slots", (torch.int32,), (n,), device)
-    a.update(n=n, num_rows=num_rows, dt=F32 if rows.dtype == torch.float32 else BF16,
-             ws=_shaped(ws, "ws", (torch.uint8,), (None,), device), ws_bytes=ws.shape[0],
-             stream=_stream(stream))
-    return a
+    if kv is None and k_idx is None:
+        raise ValueError("%s: give kv, k_idx or both" % where)
+    if (kv is None) != (kv_q8 is None) or (kv is None) != (kv_scale is None):
+        raise ValueError("%s: kv, kv_q8 and kv_scale go together" % where)
+    if (k_idx is None) != (k_codes is None) or (k_idx is None) != (k_scale is None):
+        raise ValueError("%s: k_idx, k_codes and k_scale go together" % where)
+    rows, cache = (k_idx, k_codes) if kv is None else (kv, kv_q8)
+    n, num_rows, dtype = rows.shape[0], cache.shape[0], rows.dtype
+    f32 = (torch.float32,)
+    types = (dtype,) if dtype is torch.bfloat16 or dtype is torch.float32 else ()
+    p = kq = ks = q = kc = sc = None
+    kv_step, k_step = 576, 128
+    if kv is not None:
+        p, kv_step = _rows_of(kv, "kv", types, 576, n, device)
+        kq = _dense(kv_q8, "kv_q8", (torch.uint8,), (num_rows, Q8_ROW_BYTES), device)
+        ks = _dense(kv_scale, "kv_scale", f32, (num_rows,), device)
+    if k_idx is not None:
+        q, k_step = _rows_of(k_idx, "k_idx", types, 128, n, device)
+        kc = _dense(k_codes, "k_codes", (torch.uint8, torch.float8_e4m3fn), (num_rows, 128), device)
+        sc = _dense(k_scale, "k_scale", f32, (num_rows,), device)
+    at = None if slots is None else _dense(slots, "slots", (torch.int32,), (n,), device)
+    w, w_bytes = _workspace(ws, device)
+    return device, p, kv_step, q, k_step, F32 if dtype is torch.float32 else BF16, n, at, kq, ks, kc, sc, num_rows, w, w_bytes
 
 
 def cache_write_q8(slots, ws, *, kv=None, kv_q8=None, kv_scale=None, k_idx=None, k_codes=None,
@@ -497,20 +512,20 @@ def cache_write_q8(slots, ws, *, kv=None, kv_q8=None, kv_scale=None, k_idx=None,
     the caches kv_q8 [num_rows, 640] uint8 with kv_scale [num_rows], k_codes
     [num_rows, 128] with k_scale [num_rows].  -1 skips a row; slots None: row
     n is cache row n.  No two rows may name the same slot."""
-    a = _q8_rows("cache_write_q8", slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale, stream)
-    _check(lib().ic_cache_write_q8(a["kv"], a["kvs"], a["ki"], a["kis"], a["dt"], a["n"], a["slots"],
-                                   a["kq"], a["ks"], a["kc"], a["ksc"], a["num_rows"], a["ws"],
-                                   a["ws_bytes"], a["stream"]), "ic_cache_write_q8")
+    device, kv, kvs, ki, kis, dt, n, at, kq, ks, kc, sc, num_rows, w, wb = _q8_rows(
+        "cache_write_q8", slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale)
+    _check(lib().ic_cache_write_q8(kv, kvs, ki, kis, dt, n, at, kq, ks, kc, sc, num_rows, w, wb,
+                                   _current(device, stream)), "ic_cache_write_q8")
 
 
 def cache_read_q8(slots, ws, *, kv=None, kv_q8=None, kv_scale=None, k_idx=None, k_codes=None,
                   k_scale=None, stream=None) -> None:
     """The reverse of cache_write_q8: rows slots[n] of the caches into kv
     [n, 576] and/or k_idx [n, 128]; -1 gives a row of zeros."""
-    a = _q8_rows("cache_read_q8", slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale, stream)
-    _check(lib().ic_cache_read_q8(a["kq"], a["ks"], a["kc"], a["ksc"], a["num_rows"], a["n"],
-                                  a["slots"], a["dt"], a["kv"], a["kvs"], a["ki"], a["kis"], a["ws"],
-                                  a["ws_bytes"], a["stream"]), "ic_cache_read_q8")
+    device, kv, kvs, ki, kis, dt, n, at, kq, ks, kc, sc, num_rows, w, wb = _q8_rows(
+        "cache_read_q8", slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale)
+    _check(lib().ic_cache_read_q8(kq, ks, kc, sc, num_rows, n, at, dt, kv, kvs, ki, kis, w, wb,
+                                  _current(device, stream)), "ic_cache_read_q8")
 
 
 def tree_attn_q8_workspace_size(pr: PagedRows, k: int, Hq: int) -> int:
@@ -528,14 +543,15 @@ def tree_attn_q8_paged(q, kv_q8, kv_scale, idx, pr: PagedRows, scale: float, out
     device = torch.cuda.current_device()
     B, Lq, rows = pr.B, pr.Lq, pr.num_pages * pr.page_size
     Hq, k = q.shape[-2] if q.dim() == 4 else 0, 0 if idx is None else idx.shape[-1]
-    _need(idx is None or k > 0, "idx: names no position; None stands for every position")
+    if idx is not None and k == 0:
+        raise ValueError("idx: names no position; None stands for every position")
+    bf16 = (torch.bfloat16,)
+    w, w_bytes = _workspace(ws, device)
     _check(lib().ic_tree_attn_q8_paged(
-        _shaped(q, "q", (torch.bfloat16,), (B, Lq, None, 576), device),
-        _shaped(kv_q8, "kv_q8", (torch.uint8,), (rows, Q8_ROW_BYTES), device),
-        _shaped(kv_scale, "kv_scale", (torch.float32,), (rows,), device),
-        None if idx is None else _shaped(idx, "idx", (torch.int32,), (B, Lq, None), device), k,
-        None if tree is None else _shaped(tree, "tree", (torch.int64,), (B, Lq), device),
-        ctypes.byref(pr), Hq, float(scale),
-        _shaped(out, "out", (torch.bfloat16,), (B, Lq, Hq, 512), device),
-        _shaped(ws, "ws", (torch.uint8,), (None,), device), ws.shape[0], _stream(stream)),
-        "ic_tree_attn_q8_paged")
+        _dense(q, "q", bf16, (B, Lq, Hq, 576), device),
+        _dense(kv_q8, "kv_q8", (torch.uint8,), (rows, Q8_ROW_BYTES), device),
+        _dense(kv_scale, "kv_scale", (torch.float32,), (rows,), device),
+        None if idx is None else _dense(idx, "idx", (torch.int32,), (B, Lq, k), device), k,
+        None if tree is None else _dense(tree, "tree", (torch.int64,), (B, Lq), device),
+        ctypes.byref(pr), Hq, float(scale), _dense(out, "out", bf16, (B, Lq, Hq, 512), device),
+        w, w_bytes, _current(device, stream)), "ic_tree_attn_q8_paged")

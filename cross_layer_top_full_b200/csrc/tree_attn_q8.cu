@@ -31,17 +31,19 @@
 // 64 of the block's 128 keys whole (for Q K^T) and half of the value columns
 // of all 128 (for P V): an M = 128 product of a pair takes its B operand in
 // two halves, split by keys for the one and by columns for the other.
-//   warps 0-7   softmax (thread = row x 32 keys), conversion of Q, epilogue
-//   warps 8-11  copy the block's rows: 8 and 9 K, 10 and 11 V, 16 bytes a lane
+//   warps 0-15  softmax, two groups of eight that take the blocks in turn (each
+//               with its own S buffer; thread = row x 32 keys), conversion of
+//               Q, epilogue
+//   warps 16-19 copy the block's rows: two K, two V, 16 bytes a lane
 //               (cp.async, 128 adjacent bytes per row and eight lanes; a row
 //               that nobody may see is filled with zeros), or one TMA box per
 //               64 rows where a block is 128 consecutive rows
-//   warps 12-13 resolve positions to cache rows, scales and masks, a block
+//   warps 20-21 resolve positions to cache rows, scales and masks, a block
 //               each in turn, ahead of the copies (a ring of three blocks)
-//   warp 14     rank 0: issues the MMAs: S(j+1) before P V(j), so that the
+//   warp 22     rank 0: issues the MMAs: S(j+1) before P V(j), so that the
 //               softmax of a block runs under the next block's Q K^T;
 //               rank 1: passes on that its own operands are in place
-//   warp 15     idle (it completes a warpgroup, for setmaxnreg)
+//   warp 23     idle (it completes a warpgroup)
 // Tensor memory: O 256 columns, two S buffers of 64, Q's bfloat16 columns 32,
 // one of Q's eight 8-bit slices 32.  Shared memory: seven slices of Q 56 KB,
 // K 2 x 40 KB, V 2 x 32 KB, P 16 KB, the ring 6 KB.
@@ -79,16 +81,13 @@ struct Info {                                 // one block, resolved
     int pad[3];
 };
 constexpr int OFF_INFO = OFF_P + 2 * ATOM;
-constexpr int OFF_XM = OFF_INFO + RING * (int)sizeof(Info);   // [2][4][64] float: row maxima
-constexpr int OFF_XL = OFF_XM + 2 * 4 * HROWS * 4;    // [4][64] float: row sums
-constexpr int OFF_SQ = OFF_XL + 4 * HROWS * 4;        // [64] float: scales of Q's rows
+constexpr int OFF_XM = OFF_INFO + RING * (int)sizeof(Info);   // [2 groups][4][64] float: row maxima
+constexpr int OFF_XL = OFF_XM;                        // [8][64] float: row sums, between units
+constexpr int OFF_MR = OFF_XM + 2 * 4 * HROWS * 4;    // [2][64] float: running maxima after a block
+constexpr int OFF_SQ = OFF_MR + 2 * HROWS * 4;        // [64] float: scales of Q's rows
 constexpr int OFF_BARS = OFF_SQ + HROWS * 4;
-constexpr int SOFT_WARPS = 8, W_COPY = 8, W_RES = 12, W_MMA = 14;
-constexpr int THREADS = 32 * 16;
-// Registers per thread after the warpgroups re-balance them: launched at 128,
-// the shares add up to the same total, 4 x 32 x (2 x 184 + 2 x 72) = 65536.
-constexpr int REGS_SMALL = 72, REGS_LARGE = 184;
-static_assert(4 * 32 * (2 * REGS_SMALL + 2 * REGS_LARGE) == THREADS * 128, "register shares");
+constexpr int GROUP_WARPS = 8, SOFT_WARPS = 16, W_COPY = 16, W_RES = 20, W_MMA = 22;
+constexpr int THREADS = 32 * 24;
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_QR = 384, TM_QL = 416;
 constexpr int TMEM_COLS = 512;
 constexpr int MAX_PAIRS = 74;                 // CTA pairs of 148 SMs
@@ -194,7 +193,12 @@ __device__ __forceinline__ Rows unit_rows(const Args& a, int b, int u) {
 }
 
 // ------------------------------------------------------------------ small helpers
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// Barriers of the softmax warps: of one group, of both, and the handing over of
+// the running maxima from the group of a block to that of the next.
+__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 256;" ::"r"(1 + g) : "memory"); }
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 3, 512;" ::: "memory"); }
+__device__ __forceinline__ void hand_over(int to) { asm volatile("bar.arrive %0, 512;" ::"r"(4 + to) : "memory"); }
+__device__ __forceinline__ void take_over(int g) { asm volatile("bar.sync %0, 512;" ::"r"(4 + g) : "memory"); }
 __device__ __forceinline__ uint64_t f2(float a, float b) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -232,26 +236,14 @@ __device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, ui
     lo = __nv_cvt_float2_to_fp8x2(make_float2(a - h.x, b - h.y), __NV_SATFINITE, __NV_E5M2);
 }
 
-// Four scaled query values (two bfloat16 pairs) as e4m3 numbers and e4m3
-// numbers for what they leave.  An infinity becomes a NaN (its row is lost).
-__device__ __forceinline__ float4 scaled4(uint32_t p0, uint32_t p1, float inv) {
-    float4 v = make_float4(__uint_as_float(p0 << 16) * inv, __uint_as_float(p0 & 0xffff0000u) * inv,
-                           __uint_as_float(p1 << 16) * inv, __uint_as_float(p1 & 0xffff0000u) * inv);
-    v.x += v.x - v.x; v.y += v.y - v.y; v.z += v.z - v.z; v.w += v.w - v.w;
-    return v;
-}
-__device__ __forceinline__ uint32_t high4(float4 v) {
-    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v.x, v.y), __NV_SATFINITE, __NV_E4M3) |
-           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v.z, v.w), __NV_SATFINITE, __NV_E4M3) << 16;
-}
-__device__ __forceinline__ uint32_t low4(float4 v, uint32_t hi) {
-    const float2 a = decode2(hi), b = decode2(hi >> 16);
-    return high4(make_float4(v.x - a.x, v.y - a.y, v.z - b.x, v.w - b.y));
-}
-
-// Largest finite magnitude of a bfloat16 pair, as float32 bits.
-__device__ __forceinline__ uint32_t pair_max(uint32_t p) {
-    return max(finite_abs_bits(__uint_as_float(p << 16)), finite_abs_bits(__uint_as_float(p & 0xffff0000u)));
+// Two query values (a bfloat16 pair) divided by their row's scale, as e4m3
+// numbers and e4m3 numbers for what they leave.  By way of float16, which holds
+// a bfloat16 in [-448, 448] down to 2^-24 exactly, as it does the rest.
+__device__ __forceinline__ void split_query(uint32_t p, float inv, uint32_t& hi, uint32_t& lo) {
+    const __half2 h = __floats2half2_rn(__uint_as_float(p << 16) * inv, __uint_as_float(p & 0xffff0000u) * inv);
+    hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
+    const __half2 d = __hsub2(h, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
+    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(d), __NV_SATFINITE, __NV_E4M3);
 }
 
 // Bits of the 32 positions from s0 on that a row sees by its tree mask.
@@ -271,13 +263,15 @@ __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // A partial result of a unit: O of one thread (row (warp & 1) * 32 + lane of
-// CTA rank) in 16-byte pieces i = 0..7 of 32 columns c = 0..3 from
+// CTA rank) in 16-byte pieces i = 0..7 of 32 columns c = 0..1 from
 // part_col(warp, c) on, so that a warp writes and reads 512 adjacent bytes.
 constexpr int PART = MROWS * DV / 4;
 __device__ __forceinline__ int64_t part_at(int slot, int rank, int warp, int c, int i, int lane) {
-    return (int64_t)slot * PART + ((((rank * 8 + warp) * 4 + c) * 8 + i) * 32 + lane);
+    return (int64_t)slot * PART + ((((rank * 16 + warp) * 2 + c) * 8 + i) * 32 + lane);
 }
-__device__ __forceinline__ int part_col(int warp, int c) { return 256 * (warp >> 2) + 128 * ((warp >> 1) & 1) + 32 * c; }
+__device__ __forceinline__ int part_col(int warp, int c) {
+    return 256 * (warp >> 3) + 128 * ((warp >> 1) & 1) + 64 * ((warp >> 2) & 1) + 32 * c;
+}
 
 // A warp's share of a tile: 4 * GROUPS rows (rows[], -1: zeros) of ATOMS x
 // 128 bytes, STEP bytes apart in the cache row, DST bytes apart in the tile;
@@ -303,50 +297,51 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int row0, const uint8_t*
 }
 
 // ------------------------------------------------------------------ Q of a unit
-// The 64 rows of this CTA, 256 threads: a warp takes 8 rows, a lane 16 of the
-// coded columns.  What goes to tensor memory (lane = row) passes through the
-// P tiles, which are free once P V of block j - 1 is complete.  Returns the
-// scale of this thread's row.
+// The 64 rows of this CTA, 512 threads: a warp takes 4 rows, a lane 16 of the
+// coded columns and 8 of the others.  What goes to tensor memory (lane = row)
+// passes through the P tiles, which are free once P V of block j - 1 is
+// complete.  A row with an infinity or a NaN becomes NaN as a whole (its
+// outputs are).  Returns the scale of this thread's row.
 __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t* smem, Bars& s, uint32_t rank,
                                            uint32_t tmem, uint32_t lane_base, uint32_t j) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* sq = reinterpret_cast<float*>(smem + OFF_SQ);
-    const int64_t first = r.first + rank * HROWS;
+    const __nv_bfloat16* q = a.q + (r.first + rank * HROWS) * KVW;
     const int rows = r.rows - (int)rank * HROWS;
-    uint4 v[8][2], rest[2];
+    uint4 v[4][2], rest;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int row = warp * 8 + i;
-        const uint4* p = reinterpret_cast<const uint4*>(a.q + (first + row) * KVW + lane * 16);
+    for (int i = 0; i < 4; ++i) {
+        const int row = warp * 4 + i;
+        const uint4* p = reinterpret_cast<const uint4*>(q + row * KVW + lane * 16);
         const bool ok = row < rows;
         v[i][0] = ok ? __ldg(p) : make_uint4(0u, 0u, 0u, 0u);
         v[i][1] = ok ? __ldg(p + 1) : make_uint4(0u, 0u, 0u, 0u);
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = warp * 8 + i * 4 + (lane >> 3);
-        rest[i] = row < rows ? __ldg(reinterpret_cast<const uint4*>(a.q + (first + row) * KVW + DV) + (lane & 7))
-                             : make_uint4(0u, 0u, 0u, 0u);
+    {
+        const int row = warp * 4 + (lane >> 3);
+        rest = row < rows ? __ldg(reinterpret_cast<const uint4*>(q + row * KVW + DV) + (lane & 7)) : make_uint4(0u, 0u, 0u, 0u);
     }
     if (j > 0) warp_wait(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, a.status, &s.abort, 8);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int row = warp * 8 + i;
+    for (int i = 0; i < 4; ++i) {
+        const int row = warp * 4 + i;
+        const uint32_t u[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
         uint32_t m = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            m = max(m, max(max(pair_max(v[i][h].x), pair_max(v[i][h].y)), max(pair_max(v[i][h].z), pair_max(v[i][h].w))));
-        const int e = scale_exponent(__reduce_max_sync(0xffffffffu, m));
-        const float inv = exp2_int(-e);
+        for (int k = 0; k < 8; ++k) m = max(m, max(u[k] & 0x7fff0000u, (u[k] << 16) & 0x7fff0000u));
+        m = __reduce_max_sync(0xffffffffu, m);
+        const bool finite = m < 0x7f800000u;
+        const int e = finite ? scale_exponent(m) : 0;
+        const float inv = finite ? exp2_int(-e) : __uint_as_float(0x7fffffffu);
         if (lane == 0) sq[row] = exp2_int(e);
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float4 x = scaled4(v[i][h].x, v[i][h].y, inv), y = scaled4(v[i][h].z, v[i][h].w, inv);
-            hi[2 * h] = high4(x);
-            hi[2 * h + 1] = high4(y);
-            lo[2 * h] = low4(x, hi[2 * h]);
-            lo[2 * h + 1] = low4(y, hi[2 * h + 1]);
+        for (int k = 0; k < 4; ++k) {
+            uint32_t h0, l0, h1, l1;
+            split_query(u[2 * k], inv, h0, l0);
+            split_query(u[2 * k + 1], inv, h1, l1);
+            hi[k] = h0 | h1 << 16;
+            lo[k] = l0 | l1 << 16;
         }
         const int at = row * 128 + (((lane & 7) ^ (row & 7)) << 4);
         *reinterpret_cast<uint4*>(smem + OFF_Q + (lane >> 3) * ATOM + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -354,11 +349,10 @@ __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t
             make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = warp * 8 + i * 4 + (lane >> 3);
+    {
+        const int row = warp * 4 + (lane >> 3);
         const float inv = 1.f / sq[row];
-        const uint32_t u[4] = {rest[i].x, rest[i].y, rest[i].z, rest[i].w};
+        const uint32_t u[4] = {rest.x, rest.y, rest.z, rest.w};
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -367,15 +361,16 @@ __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t
             make_uint4(w[0], w[1], w[2], w[3]);
     }
     soft_sync();
-    // to tensor memory: the last slice of lo (warps 4-7), the bfloat16 columns (warps 0-3)
-    const int row = (warp & 1) * 32 + lane;
-    uint32_t w[32];
+    // to tensor memory, 64 bytes a thread: the bfloat16 columns (warps 0-7), the last slice of lo (8-15)
+    const int row = (warp & 1) * 32 + lane, part = (warp >> 2) & 1;
+    uint32_t w[16];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        const uint4 x = *reinterpret_cast<const uint4*>(smem + OFF_P + (warp < 4 ? ATOM : 0) + row * 128 + ((c ^ (row & 7)) << 4));
+    for (int c = 0; c < 4; ++c) {
+        const uint4 x = *reinterpret_cast<const uint4*>(smem + OFF_P + (warp < 8 ? ATOM : 0) + row * 128 +
+                                                        (((part * 4 + c) ^ (row & 7)) << 4));
         w[4 * c] = x.x; w[4 * c + 1] = x.y; w[4 * c + 2] = x.z; w[4 * c + 3] = x.w;
     }
-    tmem_st32(tmem + lane_base + (warp < 4 ? TM_QR : TM_QL), w);
+    tmem_st16(tmem + lane_base + (warp < 8 ? TM_QR : TM_QL) + 16 * part, w);
     tmem_st_wait();
     fence_async_smem();
     tc_fence_before();
@@ -399,11 +394,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
 
     if (threadIdx.x == 0) {
         mbar_init(&s.q_full, SOFT_WARPS);
-        mbar_init(&s.p_full, SOFT_WARPS);
+        mbar_init(&s.p_full, GROUP_WARPS);
         mbar_init(&s.drain, 1);
         for (int i = 0; i < RING; ++i) {
             mbar_init(&s.info_full[i], 1);
-            mbar_init(&s.info_free[i], SOFT_WARPS + 4);
+            mbar_init(&s.info_free[i], GROUP_WARPS + 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.k_full[i], 64);
@@ -465,73 +460,84 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
     Walk w;
     w.start(a, s);
 
-    if (warp < SOFT_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REGS_LARGE) : "memory");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_SMALL) : "memory");
     if (warp < SOFT_WARPS) {
         // ------------------------------------------------ softmax, Q, epilogue
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const int grp = warp >> 2;                  // which 32 of a buffer's 64 columns
+        const int group = warp >> 3;                // takes the blocks j with j & 1 == group
+        const int cols = (warp >> 2) & 1;           // which 32 of a buffer's 64 columns
         const int half = (warp >> 1) & 1;           // which 64 of the block's keys
         const int row = (warp & 1) * 32 + lane;
-        const int kw = half * 2 + grp;              // which 32 of the block's keys
-        const int part = kw;                        // of the four threads of a row
-        float* xl = reinterpret_cast<float*>(smem + OFF_XL);
+        const int kw = half * 2 + cols;             // which 32 of the block's keys
+        float* xm = reinterpret_cast<float*>(smem + OFF_XM) + group * (4 * HROWS) + row;
+        float* xl = reinterpret_cast<float*>(smem + OFF_XL) + row;
+        float* mr = reinterpret_cast<float*>(smem + OFF_MR) + row;
         uint8_t* p_hi = smem + OFF_P + row * 128;
         const int sw = row & 7;
         uint32_t j = 0, slot = 0, turn = 0;         // block j is use `turn` of ring slot `slot`
-        Rows r{};
-        float sq = 0.f;
         const int m = (int)rank * HROWS + row;      // query row of a unit
-        Rows done{};
-        float mref = -INFINITY, l = 0.f;
+        Rows r{}, done{};
+        float sq = 0.f, mref = -INFINITY, l = 0.f;
         bool whole = false;
         int part_slot = 0;
         while (true) {
-            // this unit's Q, then the results of the unit before
+            // sums of the unit before, this unit's Q, results of the unit before
+            if (j > 0) {
+                soft_sync();
+                const float mlast = mr[((j - 1) & 1) * HROWS];
+                xl[(group * 4 + kw) * HROWS] = mref == mlast ? l : l * ex2_approx(mref - mlast);
+                mref = mlast;
+                soft_sync();
+                l = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) l += xl[i * HROWS];
+            }
             if (w.left > 0) {
                 r = unit_rows(a, w.b, w.u);
                 sq = convert_q(a, r, smem, s, rank, tmem, lane_base, j);
             }
             if (j > 0) {
-                xl[part * HROWS + row] = l;
-                soft_sync();
-                l = (xl[row] + xl[HROWS + row]) + (xl[2 * HROWS + row] + xl[3 * HROWS + row]);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const bool ok = warp_wait(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, status, abort, 9);
                 tc_fence_after();
-                uint8_t* stage = smem + OFF_P + warp * 2048;       // 32 rows x 64 bytes
+                if (w.left > 0) soft_sync();            // the staging area below is that of convert_q
+                uint8_t* stage = smem + OFF_P + warp * 1024;       // 32 rows x 32 bytes
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     uint32_t t[32];
-                    tmem_ld32(tmem + lane_base + TM_O + 128 * grp + 32 * c, t);
+                    tmem_ld32(tmem + lane_base + TM_O + 64 * (warp >> 2) + 32 * c, t);
                     tmem_ld_wait();
                     if (whole) {
-                        // through shared memory, so that four lanes write 64 adjacent bytes of a row
+                        // through shared memory, so that two lanes write 32 adjacent bytes of a row
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t u[4];
+                        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                u[k] = bf16_pair(__uint_as_float(t[8 * i + 2 * k]) * inv, __uint_as_float(t[8 * i + 2 * k + 1]) * inv);
-                            *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t u[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    u[k] = bf16_pair(__uint_as_float(t[16 * h + 8 * i + 2 * k]) * inv,
+                                                     __uint_as_float(t[16 * h + 8 * i + 2 * k + 1]) * inv);
+                                *reinterpret_cast<uint4*>(stage + lane * 32 + ((i ^ ((lane >> 2) & 1)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+                            }
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int rr = 16 * i + (lane >> 1), mm = (int)rank * HROWS + (warp & 1) * 32 + rr;
+                                const uint4 o = *reinterpret_cast<const uint4*>(stage + rr * 32 + (((lane & 1) ^ ((rr >> 2) & 1)) << 4));
+                                if (ok && mm < done.rows)
+                                    *(reinterpret_cast<uint4*>(a.out + (done.first + mm) * DV + part_col(warp, c)) + 2 * h + (lane & 1)) = o;
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int rr = 8 * i + (lane >> 2), mm = (int)rank * HROWS + (warp & 1) * 32 + rr;
-                            const uint4 o = *reinterpret_cast<const uint4*>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-                            if (ok && mm < done.rows)
-                                *(reinterpret_cast<uint4*>(a.out + (done.first + mm) * DV + part_col(warp, c)) + (lane & 3)) = o;
-                        }
-                        __syncwarp();
-                    } else if (ok) {
+                    } else if (ok && m < done.rows) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             a.part_o[part_at(part_slot, rank, warp, c, i, lane)] = make_uint4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
                     }
                 }
-                if (!whole && ok && part == 0) a.part_ml[part_slot * MROWS + m] = make_float2(mref, l);
+                if (!whole && ok && m < done.rows && group == 0 && kw == 0) a.part_ml[part_slot * MROWS + m] = make_float2(mref, l);
                 tc_fence_before();
+                if (w.left > 0) soft_sync();            // P goes there next
             }
             if (w.left <= 0) break;
             const int n = w.count(), len = seq_len(a, w.b), ctx = len - a.Lq;
@@ -543,31 +549,37 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             }
             const float arow = sq * a.scale_log2;
             const uint64_t a2 = f2(arow, arow);
-            mref = -INFINITY;
+            mref = -INFINITY;       // what this group's l is relative to
             l = 0.f;
             for (int x = 0; x < n; ++x, ++j) {
                 const uint32_t buf = j & 1, ph = (j >> 1) & 1;
+                if (buf != (uint32_t)group) {
+                    if (++slot == RING) { slot = 0; ++turn; }
+                    continue;
+                }
                 const int s0 = (w.t + x) * NB;              // the block's first entry
                 warp_wait(&s.info_full[slot], turn & 1, status, abort, 5);
                 const Info& info = reinterpret_cast<const Info*>(smem + OFF_INFO)[slot];
                 warp_wait(&s.s_full[buf], ph, status, abort, 6);
                 tc_fence_after();
-                uint32_t t[32];
-                tmem_ld32(tmem + lane_base + TM_S + 64 * buf + 32 * grp, t);
-                const float4* g4 = reinterpret_cast<const float4*>(info.scale) + kw * 8;
+                float y[32];
+                {
+                    uint32_t t[32];
+                    tmem_ld32(tmem + lane_base + TM_S + 64 * buf + 32 * cols, t);
+                    tmem_ld_wait();
+                    const float4* g4 = reinterpret_cast<const float4*>(info.scale) + kw * 8;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float4 g = g4[c], lg = g4[NB / 4 + c];
+                        const float2 u = f2_split(ffma2(fmul2(f2(__uint_as_float(t[4 * c]), __uint_as_float(t[4 * c + 1])), a2),
+                                                        f2(g.x, g.y), f2(lg.x, lg.y)));
+                        const float2 v = f2_split(ffma2(fmul2(f2(__uint_as_float(t[4 * c + 2]), __uint_as_float(t[4 * c + 3])), a2),
+                                                        f2(g.z, g.w), f2(lg.z, lg.w)));
+                        y[4 * c] = u.x; y[4 * c + 1] = u.y; y[4 * c + 2] = v.x; y[4 * c + 3] = v.y;
+                    }
+                }
                 uint32_t seen = info.seen[kw];
                 if (dense) seen &= tree_bits(mask, s0 + kw * 32 - ctx);
-                tmem_ld_wait();
-                float y[32];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float4 g = g4[c], lg = g4[NB / 4 + c];
-                    const float2 u = f2_split(ffma2(fmul2(f2(__uint_as_float(t[4 * c]), __uint_as_float(t[4 * c + 1])), a2),
-                                                    f2(g.x, g.y), f2(lg.x, lg.y)));
-                    const float2 v = f2_split(ffma2(fmul2(f2(__uint_as_float(t[4 * c + 2]), __uint_as_float(t[4 * c + 3])), a2),
-                                                    f2(g.z, g.w), f2(lg.z, lg.w)));
-                    y[4 * c] = u.x; y[4 * c + 1] = u.y; y[4 * c + 2] = v.x; y[4 * c + 3] = v.y;
-                }
                 if (seen != 0xffffffffu) {
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
@@ -577,23 +589,29 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
                     mx = fmaxf(mx, fmaxf(fmaxf(y[c], y[c + 8]), fmaxf(y[c + 16], y[c + 24])));
-                float* xm = reinterpret_cast<float*>(smem + OFF_XM) + buf * (4 * HROWS);
-                xm[part * HROWS + row] = mx;
-                soft_sync();
-                mx = fmaxf(fmaxf(xm[row], xm[HROWS + row]), fmaxf(xm[2 * HROWS + row], xm[3 * HROWS + row]));
-                const bool grow = mx > mref + SLACK;
-                const float mnew = grow ? mx : mref;
-                const float factor = grow ? ex2_approx(mref - mnew) : 1.f;   // 0 from -inf
+                xm[kw * HROWS] = mx;
+                group_sync(group);
+                mx = fmaxf(fmaxf(xm[0], xm[HROWS]), fmaxf(xm[2 * HROWS], xm[3 * HROWS]));
+                float mprev = -INFINITY;                    // the maximum that O is relative to
+                if (x > 0) {
+                    take_over(group);
+                    mprev = mr[(buf ^ 1) * HROWS];
+                }
+                const bool grow = mx > mprev + SLACK;
+                const float mnew = grow ? mx : mprev;
+                if (kw == 0) mr[buf * HROWS] = mnew;
+                if (x + 1 < n) hand_over(group ^ 1);
                 const float off = mnew == -INFINITY ? 0.f : TOP - mnew;
                 const uint64_t off2 = f2(off, off);
                 uint64_t l2 = f2(0.f, 0.f);
                 uint32_t hi[8], lo[8];
+                const float4* inv4 = reinterpret_cast<const float4*>(info.inv) + kw * 8;
 #pragma unroll
                 for (int c = 0; c < 32; c += 4) {
                     const float2 u = f2_split(fadd2(f2(y[c], y[c + 1]), off2));
                     const float2 v = f2_split(fadd2(f2(y[c + 2], y[c + 3]), off2));
                     const float e0 = ex2_approx(u.x), e1 = ex2_approx(u.y), e2 = ex2_approx(v.x), e3 = ex2_approx(v.y);
-                    const float4 inv = g4[2 * (NB / 4) + c / 4];
+                    const float4 inv = inv4[c / 4];
                     l2 = ffma2(f2(e0, e1), f2(inv.x, inv.y), l2);
                     l2 = ffma2(f2(e2, e3), f2(inv.z, inv.w), l2);
                     uint32_t h0, h1, r0, r1;
@@ -603,17 +621,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                     lo[c / 4] = r0 | r1 << 16;
                 }
                 const float2 ls = f2_split(l2);
-                l = l * factor + (ls.x + ls.y);
+                l = (mref == mnew ? l : l * ex2_approx(mref - mnew)) + (ls.x + ls.y);
+                mref = mnew;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.info_free[slot]);
                 if (++slot == RING) { slot = 0; ++turn; }
-                mref = mnew;
                 if (j > 0) warp_wait(&s.pv_done[buf ^ 1], ((j - 1) >> 1) & 1, status, abort, 7);
                 if (x > 0 && __any_sync(0xffffffffu, grow)) {
+                    const float factor = grow ? ex2_approx(mprev - mnew) : 1.f;   // 0 from -inf
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 8; ++c) {
-                        const uint32_t addr = tmem + lane_base + TM_O + 128 * grp + 16 * c;
+                        const uint32_t addr = tmem + lane_base + TM_O + 128 * cols + 16 * c;
                         uint32_t o[16];
                         tmem_ld16(addr, o);
                         tmem_ld_wait();
@@ -634,8 +653,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                     // not: its NaN codes become 0 here, so that 0 weights
                     // leave no NaN; the weights of the rows that see it are
                     // NaN by themselves.
-                    warp_wait(&s.v_full[buf], ph, status, abort, 8);
-                    uint4* v = reinterpret_cast<uint4*>(smem + OFF_V + buf * V_STAGE) + threadIdx.x;
+                    warp_wait(&s.v_full[buf], ph, status, abort, 4);
+                    uint4* v = reinterpret_cast<uint4*>(smem + OFF_V + buf * V_STAGE) + (threadIdx.x & 255);
 #pragma unroll 1
                     for (int c = 0; c < V_STAGE / 16 / 256; ++c) {
                         const uint4 o = v[c * 256];
@@ -895,9 +914,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
 
 // ------------------------------------------------------------------ joining partial results
 // out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the runs that share
-// a unit.  A CTA takes 16 of the 32 columns c of each warp's partial result
-// (blockIdx.y = rank, c, half); units that one run covered whole have nothing
-// to join.
+// a unit.  A warp takes 16 columns of 32 rows (half a chunk of one writing
+// warp's); units that one run covered whole have nothing to join.
 __global__ void __launch_bounds__(256)
 tree_join_kernel(const __grid_constant__ Args a, int max_pairs) {
     __shared__ int range[3];
@@ -926,8 +944,9 @@ tree_join_kernel(const __grid_constant__ Args a, int max_pairs) {
     const int p0 = pair_with(n, P, begin), p1 = pair_with(n, P, end - 1);
     if (p0 == p1) return;
     const Rows r = unit_rows(a, b, u);
-    const int rank = blockIdx.y >> 3, c = (blockIdx.y >> 1) & 3, half = blockIdx.y & 1;
-    const int m = rank * HROWS + (warp & 1) * 32 + lane;
+    const int piece = blockIdx.y * 8 + warp;
+    const int rank = piece >> 6, owner = (piece >> 2) & 15, c = (piece >> 1) & 1, half = piece & 1;
+    const int m = rank * HROWS + (owner & 1) * 32 + lane;
     if (m >= r.rows) return;
     // slot of a run: 1 where the unit begins in it, 0 where it continues the unit
     const int slot0 = 2 * p0 + (run_begin(n, P, p0) > begin ? 0 : 1);
@@ -947,13 +966,13 @@ tree_join_kernel(const __grid_constant__ Args a, int max_pairs) {
         l += wgt * ml.y;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint4 v = a.part_o[part_at(slot, rank, warp, c, half * 4 + i, lane)];
+            const uint4 v = a.part_o[part_at(slot, rank, owner, c, half * 4 + i, lane)];
             o[i].x += wgt * __uint_as_float(v.x); o[i].y += wgt * __uint_as_float(v.y);
             o[i].z += wgt * __uint_as_float(v.z); o[i].w += wgt * __uint_as_float(v.w);
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint4* d = reinterpret_cast<uint4*>(a.out + (r.first + m) * DV + part_col(warp, c) + 16 * half);
+    uint4* d = reinterpret_cast<uint4*>(a.out + (r.first + m) * DV + part_col(owner, c) + 16 * half);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         d[i] = make_uint4(bf16_pair(o[2 * i].x * inv, o[2 * i].y * inv), bf16_pair(o[2 * i].z * inv, o[2 * i].w * inv),

@@ -152,11 +152,14 @@ class _Dev:
         self.strides = tuple(strides or dense)
         self.dense = self.strides == tuple(dense)
 
+    def get_device(self):
+        return self.device.index if self.is_cuda else -1
+
     def dim(self):
         return len(self.shape)
 
-    def stride(self, i=None):
-        return self.strides if i is None else self.strides[i]
+    def stride(self):
+        return self.strides
 
     def is_contiguous(self):
         return self.dense
@@ -187,10 +190,10 @@ def test_binding_checks_cache_tensors(lib, device0, call):
     refused("kv: unexpected dtype", kv=_Dev(4, 576, dtype=torch.float16))
     refused("k_idx: unexpected dtype", k_idx=_Dev(4, 128, dtype=f32))       # not kv's type
     refused("kv: expected shape", kv=_Dev(4, 512, dtype=bf))
-    refused("kv: expected rows", kv=_Dev(4, 576, dtype=bf, strides=(1, 4)))
-    refused("kv: expected rows", kv=_Dev(1, 576, dtype=bf, strides=(576, 2)), k_idx=None,
+    refused("kv: expected a contiguous tensor .* or rows", kv=_Dev(4, 576, dtype=bf, strides=(1, 4)))
+    refused("kv: expected a contiguous tensor .* or rows", kv=_Dev(1, 576, dtype=bf, strides=(576, 2)), k_idx=None,
             k_codes=None, k_scale=None)
-    refused("kv: expected rows", kv=_Dev(4, 576, dtype=bf, strides=(0, 1)))  # one row for all
+    refused("kv: expected a contiguous tensor .* or rows", kv=_Dev(4, 576, dtype=bf, strides=(0, 1)))  # one row for all
     refused("k_idx: expected shape", k_idx=_Dev(5, 128, dtype=bf))
     refused("kv_q8: expected shape", kv_q8=_Dev(8, 656))
     refused("kv_q8: expected a contiguous", kv_q8=_Dev(8, 640, strides=(1280, 1)))

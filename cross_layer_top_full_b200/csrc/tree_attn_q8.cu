@@ -32,7 +32,7 @@
 // of all 128 (for P V): an M = 128 product of a pair takes its B operand in
 // two halves, split by keys for the one and by columns for the other.
 //   warps 0-15  softmax, two groups of eight that take the blocks in turn (each
-//               with its own S buffer; thread = row x 32 keys), conversion of
+//               with an S buffer each; thread = row x 32 keys), conversion of
 //               Q, epilogue
 //   warps 16-19 copy the block's rows: two K, two V, 16 bytes a lane
 //               (cp.async, 128 adjacent bytes per row and eight lanes; a row
@@ -40,16 +40,15 @@
 //               64 rows where a block is 128 consecutive rows
 //   warps 20-21 resolve positions to cache rows, scales and masks, a block
 //               each in turn, ahead of the copies (a ring of three blocks)
-//   warp 22     rank 0: issues the MMAs: S(j+1) before P V(j), so that the
-//               softmax of a block runs under the next block's Q K^T;
-//               rank 1: passes on that its own operands are in place
-//   warp 23     idle (it completes a warpgroup)
-// Tensor memory: O 256 columns, two S buffers of 64, Q's bfloat16 columns 32,
-// one of Q's eight 8-bit slices 32.  Shared memory: seven slices of Q 56 KB,
-// K 2 x 40 KB, V 2 x 32 KB, P 16 KB, the ring 6 KB.
+//   warps 22-23 rank 0: issue the MMAs, 22 Q K^T as soon as a block's K is there
+//               and its S buffer read, 23 P V as soon as P and V are; rank 1:
+//               pass on that its own tiles have landed
+// Tensor memory, all of it: O 256 columns, two S buffers of 64, three of Q's
+// eight 8-bit slices and its bfloat16 columns 32 each.  Shared memory: five
+// slices of Q 40 KB, K 2 x 40 KB, V 2 x 32 KB, P 2 x 16 KB, the ring 6 KB.
 //
-// Every wait is bounded (sm100.cuh); sites: 1-4 copies, 5-9 softmax, 10-15
-// MMA issue, 16 resolution.
+// Every wait is bounded (sm100.cuh); sites: 1-3 copies, 4-9 and 19 softmax,
+// 10-15 and 20 MMA issue, 16 resolution.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -66,8 +65,8 @@ using namespace sm100;
 constexpr int MROWS = 128, HROWS = 64;        // query rows of a unit, of a CTA
 constexpr int NB = 128;                       // positions per block
 constexpr int ATOM = 64 * 128;                // 64 rows of 128 bytes
-constexpr int Q_SMEM = 7;                     // slices of Q in shared memory: hi 0-3, lo 0-2
-constexpr int K_STAGE = 5 * ATOM, V_STAGE = 4 * ATOM;
+constexpr int Q_SMEM = 5;                     // slices of Q in shared memory: hi 0-3, lo 0; the rest: TM_Q
+constexpr int K_STAGE = 5 * ATOM, V_STAGE = 4 * ATOM, P_STAGE = 2 * ATOM;
 constexpr int OFF_Q = 0;
 constexpr int OFF_K = OFF_Q + Q_SMEM * ATOM;
 constexpr int OFF_V = OFF_K + 2 * K_STAGE;
@@ -80,15 +79,15 @@ struct Info {                                 // one block, resolved
     int box;                                  // 128 consecutive cache rows from rows[0] on
     int pad[3];
 };
-constexpr int OFF_INFO = OFF_P + 2 * ATOM;
+constexpr int OFF_INFO = OFF_P + 2 * P_STAGE;
 constexpr int OFF_XM = OFF_INFO + RING * (int)sizeof(Info);   // [2 groups][4][64] float: row maxima
 constexpr int OFF_XL = OFF_XM;                        // [8][64] float: row sums, between units
 constexpr int OFF_MR = OFF_XM + 2 * 4 * HROWS * 4;    // [2][64] float: running maxima after a block
 constexpr int OFF_SQ = OFF_MR + 2 * HROWS * 4;        // [64] float: scales of Q's rows
 constexpr int OFF_BARS = OFF_SQ + HROWS * 4;
-constexpr int GROUP_WARPS = 8, SOFT_WARPS = 16, W_COPY = 16, W_RES = 20, W_MMA = 22;
+constexpr int GROUP_WARPS = 8, SOFT_WARPS = 16, W_COPY = 16, W_RES = 20, W_S = 22, W_PV = 23;
 constexpr int THREADS = 32 * 24;
-constexpr uint32_t TM_O = 0, TM_S = 256, TM_QR = 384, TM_QL = 416;
+constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 384, TM_QR = TM_Q + 96;   // TM_Q: lo 1-3, the bfloat16 columns
 constexpr int TMEM_COLS = 512;
 constexpr int MAX_PAIRS = 74;                 // CTA pairs of 148 SMs
 constexpr float LOG2E = 1.4426950408889634f;
@@ -97,14 +96,14 @@ constexpr float TOP = 4.f, SLACK = 4.f;       // log2 of the largest weight when
 
 struct __align__(8) Bars {
     uint64_t info_full[RING], info_free[RING];
-    uint64_t q_full;                 // Q of a unit is in place (own warps)
+    uint64_t q_full;                 // rank 0: Q of a unit is in place (both CTAs' warps)
     uint64_t k_full[2], v_full[2];   // own tiles have landed
-    uint64_t s_peer[2];              // rank 0: rank 1's K (and Q) are in place
+    uint64_t k_peer[2], v_peer[2];   // rank 0: rank 1's tiles have landed
     uint64_t s_full[2];              // S of a block is complete: K stage free
-    uint64_t p_full;                 // P of a block is in place (own warps)
-    uint64_t pv_peer[2];             // rank 0: rank 1's P and V are in place
-    uint64_t pv_done[2];             // P V of a block is complete: V stage, P free
-    uint64_t drain;
+    uint64_t s_free[2];              // rank 0: S of a block has been read (both CTAs' warps)
+    uint64_t p_full[2];              // rank 0: P of a block is in place (both CTAs' warps)
+    uint64_t pv_done[2];             // P V of a block is complete: V stage, P stage free
+    uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
     int start_b, start_u, start_t, left;
@@ -190,6 +189,45 @@ __device__ __forceinline__ Rows unit_rows(const Args& a, int b, int u) {
     }
     r.first = (int64_t)b * a.Lq * a.Hq + r.node0;
     return r;
+}
+
+// ------------------------------------------------------------------ waits
+// Bounded like those of sm100.cuh (about a second in all), but four
+// instructions a poll: two dozen warps wait here most of the time, and longer
+// polls kept the instruction fetch from the warps that work.  Every lane waits,
+// and every lane gets the same answer.
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 4096;\n"
+        "WAIT:\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra WAIT;\n"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* abort, uint32_t site) {
+    const uint64_t t0 = globaltimer();
+    while (true) {
+        if (__all_sync(0xffffffffu, poll(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
+        if (__any_sync(0xffffffffu, globaltimer() - t0 > IC_WAIT_LIMIT_NS)) {
+            if ((threadIdx.x & 31) == 0) flag_timeout(status, site);
+            *abort = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort, uint32_t site) {
+    if (__all_sync(0xffffffffu, poll(smem_u32(bar), parity))) return true;
+    return wait_on(smem_u32(bar), parity, status, abort, site);
 }
 
 // ------------------------------------------------------------------ small helpers
@@ -303,7 +341,7 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int row0, const uint8_t*
 // complete.  A row with an infinity or a NaN becomes NaN as a whole (its
 // outputs are).  Returns the scale of this thread's row.
 __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t* smem, Bars& s, uint32_t rank,
-                                           uint32_t tmem, uint32_t lane_base, uint32_t j) {
+                                           uint32_t tmem, uint32_t lane_base, uint32_t j, uint32_t q_bar) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* sq = reinterpret_cast<float*>(smem + OFF_SQ);
     const __nv_bfloat16* q = a.q + (r.first + rank * HROWS) * KVW;
@@ -321,7 +359,7 @@ __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t
         const int row = warp * 4 + (lane >> 3);
         rest = row < rows ? __ldg(reinterpret_cast<const uint4*>(q + row * KVW + DV) + (lane & 7)) : make_uint4(0u, 0u, 0u, 0u);
     }
-    if (j > 0) warp_wait(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, a.status, &s.abort, 8);
+    if (j > 0) wait_for(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, a.status, &s.abort, 8);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = warp * 4 + i;
@@ -345,7 +383,7 @@ __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t
         }
         const int at = row * 128 + (((lane & 7) ^ (row & 7)) << 4);
         *reinterpret_cast<uint4*>(smem + OFF_Q + (lane >> 3) * ATOM + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(smem + (lane < 24 ? OFF_Q + (4 + (lane >> 3)) * ATOM : OFF_P) + at) =
+        *reinterpret_cast<uint4*>(smem + (lane < 8 ? OFF_Q + 4 * ATOM : OFF_P + ((lane >> 3) - 1) * ATOM) + at) =
             make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     __syncwarp();
@@ -357,25 +395,24 @@ __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             w[k] = bf16_pair(__uint_as_float(u[k] << 16) * inv, __uint_as_float(u[k] & 0xffff0000u) * inv);
-        *reinterpret_cast<uint4*>(smem + OFF_P + ATOM + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(smem + OFF_P + 3 * ATOM + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
             make_uint4(w[0], w[1], w[2], w[3]);
     }
     soft_sync();
-    // to tensor memory, 64 bytes a thread: the bfloat16 columns (warps 0-7), the last slice of lo (8-15)
-    const int row = (warp & 1) * 32 + lane, part = (warp >> 2) & 1;
-    uint32_t w[16];
+    // to tensor memory: warps 4t..4t+3 take tile t
+    const int row = (warp & 1) * 32 + lane, tile = warp >> 2;
+    uint32_t w[32];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const uint4 x = *reinterpret_cast<const uint4*>(smem + OFF_P + (warp < 8 ? ATOM : 0) + row * 128 +
-                                                        (((part * 4 + c) ^ (row & 7)) << 4));
+    for (int c = 0; c < 8; ++c) {
+        const uint4 x = *reinterpret_cast<const uint4*>(smem + OFF_P + tile * ATOM + row * 128 + ((c ^ (row & 7)) << 4));
         w[4 * c] = x.x; w[4 * c + 1] = x.y; w[4 * c + 2] = x.z; w[4 * c + 3] = x.w;
     }
-    tmem_st16(tmem + lane_base + (warp < 8 ? TM_QR : TM_QL) + 16 * part, w);
+    tmem_st32(tmem + lane_base + TM_Q + 32 * tile, w);
     tmem_st_wait();
     fence_async_smem();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&s.q_full);
+    if (lane == 0) mbar_arrive_remote_relaxed(q_bar);
     return sq[row];
 }
 
@@ -393,9 +430,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
     uint32_t* status = a.status;
 
     if (threadIdx.x == 0) {
-        mbar_init(&s.q_full, SOFT_WARPS);
-        mbar_init(&s.p_full, GROUP_WARPS);
-        mbar_init(&s.drain, 1);
+        mbar_init(&s.q_full, 2 * SOFT_WARPS);
         for (int i = 0; i < RING; ++i) {
             mbar_init(&s.info_full[i], 1);
             mbar_init(&s.info_free[i], GROUP_WARPS + 4);
@@ -403,16 +438,19 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.k_full[i], 64);
             mbar_init(&s.v_full[i], 64);
-            mbar_init(&s.s_peer[i], 1);
-            mbar_init(&s.pv_peer[i], 1);
+            mbar_init(&s.k_peer[i], 1);
+            mbar_init(&s.v_peer[i], 1);
+            mbar_init(&s.p_full[i], 2 * GROUP_WARPS);
+            mbar_init(&s.s_free[i], 2 * GROUP_WARPS);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.pv_done[i], 1);
+            mbar_init(&s.drain[i], 1);
         }
         s.abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&map_box);
     }
-    if (warp == W_MMA) tmem_alloc_pair<TMEM_COLS>(&s.tmem_base);
+    if (warp == W_S) tmem_alloc_pair<TMEM_COLS>(&s.tmem_base);
     pdl_wait();
     if (warp == W_RES) {             // this pair's run
         const int n = total_blocks(a), P = pairs_of(n, gridDim.x / 2), p = blockIdx.x / 2;
@@ -471,7 +509,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
         float* xm = reinterpret_cast<float*>(smem + OFF_XM) + group * (4 * HROWS) + row;
         float* xl = reinterpret_cast<float*>(smem + OFF_XL) + row;
         float* mr = reinterpret_cast<float*>(smem + OFF_MR) + row;
-        uint8_t* p_hi = smem + OFF_P + row * 128;
+        uint8_t* p_hi = smem + OFF_P + group * P_STAGE + row * 128;
+        // (the arrivals at rank 0's barriers from the other SM are relaxed: what
+        // they announce is read by the tensor core of the SM that wrote it, after
+        // the writer's fence; a release at cluster scope took 2000 cycles here)
+        const uint32_t q_bar = map_to_rank(smem_u32(&s.q_full), 0), p_bar = map_to_rank(smem_u32(&s.p_full[group]), 0);
+        const uint32_t s_bar = map_to_rank(smem_u32(&s.s_free[group]), 0);
         const int sw = row & 7;
         uint32_t j = 0, slot = 0, turn = 0;         // block j is use `turn` of ring slot `slot`
         const int m = (int)rank * HROWS + row;      // query row of a unit
@@ -493,42 +536,38 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             }
             if (w.left > 0) {
                 r = unit_rows(a, w.b, w.u);
-                sq = convert_q(a, r, smem, s, rank, tmem, lane_base, j);
+                sq = convert_q(a, r, smem, s, rank, tmem, lane_base, j, q_bar);
             }
             if (j > 0) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                const bool ok = warp_wait(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, status, abort, 9);
+                const bool ok = wait_for(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, status, abort, 9);
                 tc_fence_after();
                 if (w.left > 0) soft_sync();            // the staging area below is that of convert_q
-                uint8_t* stage = smem + OFF_P + warp * 1024;       // 32 rows x 32 bytes
+                uint8_t* stage = smem + OFF_P + warp * 2048;       // 32 rows x 64 bytes
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
                     uint32_t t[32];
                     tmem_ld32(tmem + lane_base + TM_O + 64 * (warp >> 2) + 32 * c, t);
                     tmem_ld_wait();
                     if (whole) {
-                        // through shared memory, so that two lanes write 32 adjacent bytes of a row
+                        // through shared memory, so that four lanes write 64 adjacent bytes of a row
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t u[4];
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                uint32_t u[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    u[k] = bf16_pair(__uint_as_float(t[16 * h + 8 * i + 2 * k]) * inv,
-                                                     __uint_as_float(t[16 * h + 8 * i + 2 * k + 1]) * inv);
-                                *reinterpret_cast<uint4*>(stage + lane * 32 + ((i ^ ((lane >> 2) & 1)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
-                            }
-                            __syncwarp();
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int rr = 16 * i + (lane >> 1), mm = (int)rank * HROWS + (warp & 1) * 32 + rr;
-                                const uint4 o = *reinterpret_cast<const uint4*>(stage + rr * 32 + (((lane & 1) ^ ((rr >> 2) & 1)) << 4));
-                                if (ok && mm < done.rows)
-                                    *(reinterpret_cast<uint4*>(a.out + (done.first + mm) * DV + part_col(warp, c)) + 2 * h + (lane & 1)) = o;
-                            }
-                            __syncwarp();
+                            for (int k = 0; k < 4; ++k)
+                                u[k] = bf16_pair(__uint_as_float(t[8 * i + 2 * k]) * inv, __uint_as_float(t[8 * i + 2 * k + 1]) * inv);
+                            *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
                         }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int rr = 8 * i + (lane >> 2), mm = (int)rank * HROWS + (warp & 1) * 32 + rr;
+                            const uint4 o = *reinterpret_cast<const uint4*>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+                            if (ok && mm < done.rows)
+                                *(reinterpret_cast<uint4*>(a.out + (done.first + mm) * DV + part_col(warp, c)) + (lane & 3)) = o;
+                        }
+                        __syncwarp();
                     } else if (ok && m < done.rows) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -558,15 +597,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                     continue;
                 }
                 const int s0 = (w.t + x) * NB;              // the block's first entry
-                warp_wait(&s.info_full[slot], turn & 1, status, abort, 5);
+                wait_for(&s.info_full[slot], turn & 1, status, abort, 5);
                 const Info& info = reinterpret_cast<const Info*>(smem + OFF_INFO)[slot];
-                warp_wait(&s.s_full[buf], ph, status, abort, 6);
+                wait_for(&s.s_full[buf], ph, status, abort, 6);
                 tc_fence_after();
                 float y[32];
                 {
                     uint32_t t[32];
                     tmem_ld32(tmem + lane_base + TM_S + 64 * buf + 32 * cols, t);
                     tmem_ld_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote_relaxed(s_bar);
                     const float4* g4 = reinterpret_cast<const float4*>(info.scale) + kw * 8;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
@@ -626,22 +668,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.info_free[slot]);
                 if (++slot == RING) { slot = 0; ++turn; }
-                if (j > 0) warp_wait(&s.pv_done[buf ^ 1], ((j - 1) >> 1) & 1, status, abort, 7);
                 if (x > 0 && __any_sync(0xffffffffu, grow)) {
+                    // O of the blocks before this one, which P V of the block has not joined yet
                     const float factor = grow ? ex2_approx(mprev - mnew) : 1.f;   // 0 from -inf
+                    wait_for(&s.pv_done[buf ^ 1], ((j - 1) >> 1) & 1, status, abort, 7);
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        const uint32_t addr = tmem + lane_base + TM_O + 128 * cols + 16 * c;
-                        uint32_t o[16];
-                        tmem_ld16(addr, o);
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t addr = tmem + lane_base + TM_O + 128 * cols + 32 * c;
+                        uint32_t o[32];
+                        tmem_ld32(addr, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-                        tmem_st16(addr, o);
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+                        tmem_st32(addr, o);
                     }
                     tmem_st_wait();
                 }
+                if (j > 1) wait_for(&s.pv_done[buf], ((j - 2) >> 1) & 1, status, abort, 19);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int at = ((kw * 2 + c) ^ sw) << 4;
@@ -653,7 +697,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                     // not: its NaN codes become 0 here, so that 0 weights
                     // leave no NaN; the weights of the rows that see it are
                     // NaN by themselves.
-                    warp_wait(&s.v_full[buf], ph, status, abort, 4);
+                    wait_for(&s.v_full[buf], ph, status, abort, 4);
                     uint4* v = reinterpret_cast<uint4*>(smem + OFF_V + buf * V_STAGE) + (threadIdx.x & 255);
 #pragma unroll 1
                     for (int c = 0; c < V_STAGE / 16 / 256; ++c) {
@@ -669,7 +713,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.p_full);
+                if (lane == 0) mbar_arrive_remote_relaxed(p_bar);
             }
             done = r;
             whole = w.t == 0 && n == w.nt;
@@ -691,8 +735,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
         bool ok = true;
         for (int left = w.left; left > 0; --left, ++j) {
             const uint32_t buf = j & 1;
-            ok = warp_wait(&s.info_full[slot], turn & 1, status, abort, 1);
-            if (ok && j >= 2) ok = warp_wait(&freed[buf], ((j - 2) >> 1) & 1, status, abort, is_k ? 2 : 3);
+            ok = wait_for(&s.info_full[slot], turn & 1, status, abort, 1);
+            if (ok && j >= 2) ok = wait_for(&freed[buf], ((j - 2) >> 1) & 1, status, abort, is_k ? 2 : 3);
             if (!ok) break;
             const Info& info = reinterpret_cast<const Info*>(smem + OFF_INFO)[slot];
             const uint32_t dst0 = stage0 + buf * stage_bytes;
@@ -723,7 +767,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
         copy_wait_all();
         // boxes have landed before the CTA exits, whatever happened
         for (uint32_t i = j > 2 ? j - 2 : 0; i < j; ++i) mbar_wait_drain(&full[i & 1], (i >> 1) & 1, 200000000ull);
-    } else if (warp < W_MMA) {
+    } else if (warp < W_S) {
         // ------------------------------------------------ positions, scales, masks
         uint32_t j = 0;
         bool ok = true;
@@ -786,7 +830,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                     inv[i] = __uint_as_float(0x7f000000u - u);
                 }
                 const uint32_t slot = j % RING, turn = j / RING;
-                if (turn > 0) ok = warp_wait(&s.info_free[slot], (turn - 1) & 1, status, abort, 16);
+                if (turn > 0) ok = wait_for(&s.info_free[slot], (turn - 1) & 1, status, abort, 16);
                 if (!ok) break;
                 Info& info = reinterpret_cast<Info*>(smem + OFF_INFO)[slot];
                 reinterpret_cast<int4*>(info.rows)[lane] = make_int4(rows[0], rows[1], rows[2], rows[3]);
@@ -800,113 +844,101 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             }
             if (ok) w.next(a);
         }
-    } else if (warp == W_MMA) {
+    } else {
         // ------------------------------------------------ MMA issue; rank 1 passes its readiness on
         // (counts and outcomes of waits go through votes, which keeps the
-        // control flow uniform).  What rank 1 passes on never leaves its SM,
-        // whose tensor core reads it there, and its own waits and fence come
-        // first: the arrival itself needs no release at cluster scope, which
-        // took 2000 cycles a block here.
-        constexpr uint32_t id_s = idesc_f32acc(0, 0, MROWS, NB), id_r = idesc_f32acc(1, 1, MROWS, NB);
-        constexpr uint32_t id_ph = idesc_f32acc(0, 0, MROWS, 256, 0, 1), id_pl = idesc_f32acc(1, 0, MROWS, 256, 0, 1);
-        const uint64_t qd = desc_sw128(sbase + OFF_Q, 16, 1024), kd = desc_sw128(sbase + OFF_K, 16, 1024);
-        const uint64_t vd = desc_sw128(sbase + OFF_V, 16, 1024), pd = desc_sw128(sbase + OFF_P, 16, 1024);
-        const uint32_t s_peer = map_to_rank(smem_u32(&s.s_peer[0]), 0), pv_peer = map_to_rank(smem_u32(&s.pv_peer[0]), 0);
+        // control flow uniform)
         const bool leader = __any_sync(0xffffffffu, rank == 0);
-        auto lane0_wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-            bool good = true;
-            if (lane == 0) good = mbar_wait(bar, parity, status, abort, site);
-            return __all_sync(0xffffffffu, good) != 0;
-        };
-        auto lane0_wait_peer = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-            bool good = true;
-            if (lane == 0) good = mbar_wait_cluster(bar, parity, status, abort, site);
-            return __all_sync(0xffffffffu, good) != 0;
-        };
-        uint32_t unit = 0;
-        bool ok = true;
-        auto issue_s = [&](uint32_t j, bool first) {
-            const uint32_t buf = j & 1, ph = (j >> 1) & 1;
-            if (first) ok = ok && lane0_wait(&s.q_full, unit++ & 1, 10);
-            ok = ok && lane0_wait(&s.k_full[buf], ph, 11);
-            if (!ok) return;
-            fence_async_smem();
-            if (!leader) {
-                if (lane == 0) mbar_arrive_remote_relaxed(s_peer + 8 * buf);
-                return;
-            }
-            ok = lane0_wait_peer(&s.s_peer[buf], ph, 12);
-            if (!ok) return;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint32_t d = TM_S + 64 * buf;
-                const uint64_t kb = kd + buf * (K_STAGE >> 4);
-#pragma unroll 4
-                for (int c = 0; c < 16; ++c)
-                    mma_f8_pair(d, qd + (c >> 2) * (ATOM >> 4) + (c & 3) * 2, kb + (c >> 2) * (ATOM >> 4) + (c & 3) * 2, id_s, c > 0);
-#pragma unroll 4
-                for (int c = 0; c < 12; ++c)
-                    mma_f8_pair(d, qd + (4 + (c >> 2)) * (ATOM >> 4) + (c & 3) * 2, kb + (c >> 2) * (ATOM >> 4) + (c & 3) * 2, id_s, 1);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) mma_f8_ts_pair(d, TM_QL + 8 * c, kb + 3 * (ATOM >> 4) + c * 2, id_s, 1);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) mma_bf16_ts_pair(d, TM_QR + 8 * c, kb + 4 * (ATOM >> 4) + c * 2, id_r, 1);
-                mma_commit_pair(&s.s_full[buf]);
-            }
-            __syncwarp();
-        };
-        auto issue_pv = [&](uint32_t j, bool first) {
-            const uint32_t buf = j & 1, ph = (j >> 1) & 1;
-            ok = ok && lane0_wait(&s.v_full[buf], ph, 13);
-            ok = ok && lane0_wait(&s.p_full, j & 1, 14);
-            if (!ok) return;
-            fence_async_smem();
-            if (!leader) {
-                if (lane == 0) mbar_arrive_remote_relaxed(pv_peer + 8 * buf);
-                return;
-            }
-            ok = lane0_wait_peer(&s.pv_peer[buf], ph, 15);
-            if (!ok) return;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t vb = vd + buf * (V_STAGE >> 4);
-#pragma unroll 4
-                for (int c = 0; c < 8; ++c)            // hi, lo
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)        // value columns 0-255, 256-511
-                        mma_f8_pair(TM_O + 128 * h, pd + (c >> 2) * (ATOM >> 4) + (c & 3) * 2,
-                                    vb + h * (2 * ATOM >> 4) + (c & 3) * (32 * 128 >> 4), c < 4 ? id_ph : id_pl,
-                                    c > 0 || !first);
-                mma_commit_pair(&s.pv_done[buf]);
-            }
-            __syncwarp();
-        };
-        // S(j + 1) goes before P V(j) inside a unit and after it where a new
-        // unit begins (its Q is not ready earlier)
-        int js = 0, jp = 0, unit_begin = 0, unit_end = 0;      // next S, next P V; the latter's unit
         const int total = __reduce_max_sync(0xffffffffu, w.left);
-        while (ok && jp < total) {
-            if (jp == unit_end) {
-                unit_begin = unit_end;
-                unit_end += __reduce_max_sync(0xffffffffu, w.count());
-                w.next(a);
+        uint32_t unit = 0;
+        int unit_begin = 0, unit_end = 0;
+        bool ok = true;
+        if (warp == W_S) {
+            constexpr uint32_t id_s = idesc_f32acc(0, 0, MROWS, NB), id_r = idesc_f32acc(1, 1, MROWS, NB);
+            const uint64_t qd = desc_sw128(sbase + OFF_Q, 16, 1024), kd = desc_sw128(sbase + OFF_K, 16, 1024);
+            const uint32_t k_peer = map_to_rank(smem_u32(&s.k_peer[0]), 0);
+            for (int j = 0; j < total; ++j) {
+                const uint32_t buf = j & 1, ph = (j >> 1) & 1;
+                if (j == unit_end) {
+                    unit_begin = unit_end;
+                    unit_end += __reduce_max_sync(0xffffffffu, w.count());
+                    w.next(a);
+                }
+                ok = wait_for(&s.k_full[buf], ph, status, abort, 10);
+                if (!ok) break;
+                fence_async_smem();
+                if (!leader) {
+                    if (lane == 0) mbar_arrive_remote_relaxed(k_peer + 8 * buf);
+                    continue;
+                }
+                ok = wait_for(&s.k_peer[buf], ph, status, abort, 11);
+                if (j > 1) ok = ok && wait_for(&s.s_free[buf], ((j - 2) >> 1) & 1, status, abort, 20);
+                if (j == unit_begin) ok = ok && wait_for(&s.q_full, unit++ & 1, status, abort, 12);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t d = TM_S + 64 * buf;
+                    const uint64_t kb = kd + buf * (K_STAGE >> 4);
+#pragma unroll 4
+                    for (int c = 0; c < 16; ++c)
+                        mma_f8_pair(d, qd + (c >> 2) * (ATOM >> 4) + (c & 3) * 2, kb + (c >> 2) * (ATOM >> 4) + (c & 3) * 2, id_s, c > 0);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) mma_f8_pair(d, qd + 4 * (ATOM >> 4) + c * 2, kb + c * 2, id_s, 1);
+#pragma unroll 4
+                    for (int c = 0; c < 12; ++c)
+                        mma_f8_ts_pair(d, TM_Q + 8 * c, kb + (1 + (c >> 2)) * (ATOM >> 4) + (c & 3) * 2, id_s, 1);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) mma_bf16_ts_pair(d, TM_QR + 8 * c, kb + 4 * (ATOM >> 4) + c * 2, id_r, 1);
+                    mma_commit_pair(&s.s_full[buf]);
+                }
+                __syncwarp();
             }
-            if (js < unit_end && js <= jp + 1) {
-                issue_s(js, js == unit_begin);
-                ++js;
-            } else {
-                issue_pv(jp, jp == unit_begin);
-                ++jp;
+        } else {
+            constexpr uint32_t id_ph = idesc_f32acc(0, 0, MROWS, 256, 0, 1), id_pl = idesc_f32acc(1, 0, MROWS, 256, 0, 1);
+            const uint64_t vd = desc_sw128(sbase + OFF_V, 16, 1024), pd = desc_sw128(sbase + OFF_P, 16, 1024);
+            const uint32_t v_peer = map_to_rank(smem_u32(&s.v_peer[0]), 0);
+            for (int j = 0; j < total; ++j) {
+                const uint32_t buf = j & 1, ph = (j >> 1) & 1;
+                if (j == unit_end) {
+                    unit_begin = unit_end;
+                    unit_end += __reduce_max_sync(0xffffffffu, w.count());
+                    w.next(a);
+                }
+                ok = wait_for(&s.v_full[buf], ph, status, abort, 13);
+                if (!ok) break;
+                fence_async_smem();
+                if (!leader) {
+                    if (lane == 0) mbar_arrive_remote_relaxed(v_peer + 8 * buf);
+                    continue;
+                }
+                ok = wait_for(&s.v_peer[buf], ph, status, abort, 14);
+                ok = ok && wait_for(&s.p_full[buf], ph, status, abort, 15);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t vb = vd + buf * (V_STAGE >> 4), pb = pd + buf * (P_STAGE >> 4);
+#pragma unroll 4
+                    for (int c = 0; c < 8; ++c)            // hi, lo
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)        // value columns 0-255, 256-511
+                            mma_f8_pair(TM_O + 128 * h, pb + (c >> 2) * (ATOM >> 4) + (c & 3) * 2,
+                                        vb + h * (2 * ATOM >> 4) + (c & 3) * (32 * 128 >> 4), c < 4 ? id_ph : id_pl,
+                                        c > 0 || j != unit_begin);
+                    mma_commit_pair(&s.pv_done[buf]);
+                }
+                __syncwarp();
             }
         }
-        if (leader && elect_one()) mma_commit_pair(&s.drain);
-        if (lane == 0) mbar_wait_drain(&s.drain, 0, leader ? 200000000ull : 400000000ull);
+        uint64_t* drain = &s.drain[warp - W_S];
+        if (leader && elect_one()) mma_commit_pair(drain);
+        __syncwarp();
+        if (lane == 0) mbar_wait_drain(drain, 0, leader ? 200000000ull : 400000000ull);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     cluster_sync();
-    if (warp == W_MMA) {
+    if (warp == W_S) {
         tc_fence_after();
         tmem_dealloc_pair<TMEM_COLS>(tmem);
     }

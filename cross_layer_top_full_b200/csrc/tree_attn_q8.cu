@@ -270,8 +270,18 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
 // Two e4m3 numbers and two e5m2 numbers for what they leave of (a, b).
 __device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
     hi = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const float2 h = decode2(hi);
-    lo = __nv_cvt_float2_to_fp8x2(make_float2(a - h.x, b - h.y), __NV_SATFINITE, __NV_E5M2);
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3);
+    float ra, rb;
+    asm("{\n\t.reg .b16 m;\n\tmov.b16 m, 0xbc00;\n\t"            // a - hi: hi * -1 + a, exactly
+        "fma.rn.f32.f16 %0, %2, m, %4;\n\tfma.rn.f32.f16 %1, %3, m, %5;\n\t}"
+        : "=f"(ra), "=f"(rb)
+        : "h"(h.x), "h"(h.y), "f"(a), "f"(b));
+    lo = __nv_cvt_float2_to_fp8x2(make_float2(ra, rb), __NV_SATFINITE, __NV_E5M2);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // Two query values (a bfloat16 pair) divided by their row's scale, as e4m3
@@ -293,10 +303,6 @@ __device__ __forceinline__ uint32_t tree_bits(unsigned long long mask, int off) 
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {   // the rest of 16: zeros
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// This thread's arrival at `bar` once its copies so far have landed.
-__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -436,8 +442,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             mbar_init(&s.info_free[i], GROUP_WARPS + 4);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.k_full[i], 64);
-            mbar_init(&s.v_full[i], 64);
+            mbar_init(&s.k_full[i], 2);
+            mbar_init(&s.v_full[i], 2);
             mbar_init(&s.k_peer[i], 1);
             mbar_init(&s.v_peer[i], 1);
             mbar_init(&s.p_full[i], 2 * GROUP_WARPS);
@@ -621,16 +627,19 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                     }
                 }
                 uint32_t seen = info.seen[kw];
-                if (dense) seen &= tree_bits(mask, s0 + kw * 32 - ctx);
+                if (dense && s0 + NB > ctx) seen &= tree_bits(mask, s0 + kw * 32 - ctx);
                 if (seen != 0xffffffffu) {
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
                         if (!((seen >> c) & 1u)) y[c] = -INFINITY;
                 }
-                float mx = -INFINITY;
+                float mx = y[0], my = y[1];
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    mx = fmaxf(mx, fmaxf(fmaxf(y[c], y[c + 8]), fmaxf(y[c + 16], y[c + 24])));
+                for (int c = 2; c < 32; c += 4) {
+                    mx = max3(mx, y[c], y[c + 1]);
+                    if (c + 2 < 32) my = max3(my, y[c + 2], y[c + 3]);
+                }
+                mx = fmaxf(mx, my);
                 xm[kw * HROWS] = mx;
                 group_sync(group);
                 mx = fmaxf(fmaxf(xm[0], xm[HROWS]), fmaxf(xm[2 * HROWS], xm[3 * HROWS]));
@@ -723,8 +732,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
     } else if (warp < W_RES) {
         // ------------------------------------------------ copies of the tiles
         // K: this CTA's 64 keys whole, 32 rows per warp; V: its columns of all
-        // keys, 64 rows per warp.  Every lane's arrival comes with its copies;
-        // who waits for a tile orders them before its MMAs (fence_async_smem).
+        // keys, 64 rows per warp.
         const bool is_k = warp < W_COPY + 2;
         const int mine = (warp - W_COPY) & 1;
         const int stage_bytes = is_k ? K_STAGE : V_STAGE;
@@ -742,7 +750,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             const uint32_t dst0 = stage0 + buf * stage_bytes;
             const bool box = info.box != 0;
             if (box) {
-                if (lane == 0 && mine == 0) {
+                if (lane != 0) {
+                } else if (mine == 0) {
                     mbar_arrive_expect_tx(&full[buf], stage_bytes);
                     uint8_t* d = smem + (dst0 - sbase);
                     if (is_k)
@@ -758,13 +767,17 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             } else {
                 if (is_k) copy_rows<8, 5, 128, ATOM>(dst0, mine * 32, a.cache, info.rows + (int)rank * HROWS + mine * 32, lane);
                 else copy_rows<16, 2, 256, 2 * ATOM>(dst0, mine * 64, a.cache + rank * 128, info.rows + mine * 64, lane);
-                copy_arrive(&full[buf]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.info_free[slot]);
+            if (!box) {             // the other stage is not free yet: nothing else to send meanwhile
+                copy_wait_all();
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[buf]);
+            }
             if (++slot == RING) { slot = 0; ++turn; }
         }
-        copy_wait_all();
         // boxes have landed before the CTA exits, whatever happened
         for (uint32_t i = j > 2 ? j - 2 : 0; i < j; ++i) mbar_wait_drain(&full[i & 1], (i >> 1) & 1, 200000000ull);
     } else if (warp < W_S) {
@@ -866,7 +879,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 }
                 ok = wait_for(&s.k_full[buf], ph, status, abort, 10);
                 if (!ok) break;
-                fence_async_smem();
                 if (!leader) {
                     if (lane == 0) mbar_arrive_remote_relaxed(k_peer + 8 * buf);
                     continue;
@@ -906,7 +918,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 }
                 ok = wait_for(&s.v_full[buf], ph, status, abort, 13);
                 if (!ok) break;
-                fence_async_smem();
                 if (!leader) {
                     if (lane == 0) mbar_arrive_remote_relaxed(v_peer + 8 * buf);
                     continue;

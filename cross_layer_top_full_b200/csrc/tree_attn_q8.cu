@@ -122,6 +122,8 @@ struct Args {
     __nv_bfloat16* out;
     uint4* part_o;      // [2 * pairs][PART]: float32, in the order of the threads that hold them
     float2* part_ml;    // [2 * pairs][128]: running maximum, sum
+    int4* joins;        // [pairs]: the unit that ends in the pair's run and began before it: its first
+                        // query row (64 bits), rows, first pair (rows 0: there is none)
     uint32_t* status;
     int k, B, Lq, Hq, T_max, max_pages, page_size, num_pages;
     int units;          // per sequence
@@ -310,7 +312,7 @@ __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_al
 // CTA rank) in 16-byte pieces i = 0..7 of 32 columns c = 0..1 from
 // part_col(warp, c) on, so that a warp writes and reads 512 adjacent bytes.
 constexpr int PART = MROWS * DV / 4;
-__device__ __forceinline__ int64_t part_at(int slot, int rank, int warp, int c, int i, int lane) {
+__host__ __device__ constexpr int64_t part_at(int slot, int rank, int warp, int c, int i, int lane) {
     return (int64_t)slot * PART + ((((rank * 16 + warp) * 2 + c) * 8 + i) * 32 + lane);
 }
 __device__ __forceinline__ int part_col(int warp, int c) {
@@ -488,11 +490,17 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             }
         }
         if (lane == 0) {
-            const int nt = left > 0 ? blocks_of(a, b) : 1;
+            const int nt = left > 0 ? blocks_of(a, b) : 1, t = off % nt;
             s.start_b = b;
             s.start_u = off / nt;
-            s.start_t = off % nt;
+            s.start_t = t;
             s.left = left;
+            if (rank == 0) {
+                const Rows r = unit_rows(a, b, off / nt);
+                const bool ends = left > 0 && t > 0 && left >= nt - t;
+                a.joins[p] = make_int4((int)(uint32_t)r.first, (int)(r.first >> 32), ends ? r.rows : 0,
+                                       ends ? pair_with(n, P, begin - t) : 0);
+            }
         }
     }
     tc_fence_before();
@@ -957,69 +965,48 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
 
 // ------------------------------------------------------------------ joining partial results
 // out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the runs that share
-// a unit.  A warp takes 16 columns of 32 rows (half a chunk of one writing
-// warp's); units that one run covered whole have nothing to join.
+// a unit; blockIdx.x is the run in which the unit ends.  A warp takes 32 rows
+// of N 16-byte pieces (neighbours in a chunk of one writing warp), with four
+// runs' loads in flight.
+template <int N>
 __global__ void __launch_bounds__(256)
-tree_join_kernel(const __grid_constant__ Args a, int max_pairs) {
-    __shared__ int range[3];
+tree_join_kernel(const __grid_constant__ Args a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.x / a.units, u = blockIdx.x % a.units;
     pdl_trigger();
     pdl_wait();
-    if (warp == 0) {
-        const int n = total_blocks(a);
-        int begin = 0;
-        if (a.idx) {
-            begin = blockIdx.x * a.list_blocks;
-        } else {
-            for (int i = lane; i < b; i += 32) begin += blocks_of(a, i);
-            begin = __reduce_add_sync(0xffffffffu, begin) * a.units + u * blocks_of(a, b);
-        }
-        if (lane == 0) {
-            range[0] = n;
-            range[1] = begin;
-            range[2] = begin + blocks_of(a, b);
-        }
-    }
-    __syncthreads();
-    const int n = range[0], begin = range[1], end = range[2];
-    const int P = pairs_of(n, max_pairs);
-    const int p0 = pair_with(n, P, begin), p1 = pair_with(n, P, end - 1);
-    if (p0 == p1) return;
-    const Rows r = unit_rows(a, b, u);
+    const int4 join = __ldg(a.joins + blockIdx.x);
+    const int p0 = join.w, p1 = blockIdx.x;
     const int piece = blockIdx.y * 8 + warp;
-    const int rank = piece >> 6, owner = (piece >> 2) & 15, c = (piece >> 1) & 1, half = piece & 1;
+    const int at = piece % (8 / N) * N, c = piece / (8 / N) & 1, owner = piece / (16 / N) & 15, rank = piece / (256 / N);
     const int m = rank * HROWS + (owner & 1) * 32 + lane;
-    if (m >= r.rows) return;
+    if (m >= join.z) return;
     // slot of a run: 1 where the unit begins in it, 0 where it continues the unit
-    const int slot0 = 2 * p0 + (run_begin(n, P, p0) > begin ? 0 : 1);
     float top = -INFINITY;
 #pragma unroll 4
-    for (int p = p0; p <= p1; ++p) top = fmaxf(top, a.part_ml[(p == p0 ? slot0 : 2 * p) * MROWS + m].x);
-    float4 o[4];
+    for (int p = p0; p <= p1; ++p) top = fmaxf(top, __ldg(&a.part_ml[(2 * p + (p == p0)) * MROWS + m].x));
+    float4 o[N];
     float l = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+    for (int i = 0; i < N; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int p = p0; p <= p1; ++p) {
-        const int slot = p == p0 ? slot0 : 2 * p;
-        const float2 ml = a.part_ml[slot * MROWS + m];
+        const int slot = 2 * p + (p == p0);
+        const float2 ml = __ldg(a.part_ml + slot * MROWS + m);
         // a run that saw nothing of the row has weight 0 (its sum is 0, or a NaN that stays)
         const float wgt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_approx(ml.x - top);
         l += wgt * ml.y;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint4 v = a.part_o[part_at(slot, rank, owner, c, half * 4 + i, lane)];
+        for (int i = 0; i < N; ++i) {
+            const uint4 v = __ldg(a.part_o + part_at(slot, rank, owner, c, at + i, lane));
             o[i].x += wgt * __uint_as_float(v.x); o[i].y += wgt * __uint_as_float(v.y);
             o[i].z += wgt * __uint_as_float(v.z); o[i].w += wgt * __uint_as_float(v.w);
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint4* d = reinterpret_cast<uint4*>(a.out + (r.first + m) * DV + part_col(owner, c) + 16 * half);
+    const int64_t first = (int64_t)(((uint64_t)(uint32_t)join.y << 32) | (uint32_t)join.x);
+    uint2* d = reinterpret_cast<uint2*>(a.out + (first + m) * DV + part_col(owner, c) + 4 * at);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        d[i] = make_uint4(bf16_pair(o[2 * i].x * inv, o[2 * i].y * inv), bf16_pair(o[2 * i].z * inv, o[2 * i].w * inv),
-                          bf16_pair(o[2 * i + 1].x * inv, o[2 * i + 1].y * inv), bf16_pair(o[2 * i + 1].z * inv, o[2 * i + 1].w * inv));
+    for (int i = 0; i < N; ++i) d[i] = make_uint2(bf16_pair(o[i].x * inv, o[i].y * inv), bf16_pair(o[i].z * inv, o[i].w * inv));
 }
 
 // ------------------------------------------------------------------ host side
@@ -1064,7 +1051,7 @@ Plan plan(const ic_paged_rows& pr, int k, int Hq) {
 }  // namespace
 
 size_t tree_attn_q8_scratch_bytes(const ic_paged_rows& pr, int k, int Hq) {
-    return (size_t)plan(pr, k, Hq).pairs * 2 * MROWS * (DV * sizeof(float) + sizeof(float2));
+    return (size_t)plan(pr, k, Hq).pairs * (2 * MROWS * (DV * sizeof(float) + sizeof(float2)) + sizeof(int4));
 }
 
 ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_scale,
@@ -1086,6 +1073,7 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
     a.out = static_cast<__nv_bfloat16*>(out);
     a.part_o = static_cast<uint4*>(scratch);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)p.pairs * 2 * PART);
+    a.joins = reinterpret_cast<int4*>(a.part_ml + (size_t)p.pairs * 2 * MROWS);
     a.status = status;
     a.k = k;
     a.B = pr.B;
@@ -1108,7 +1096,11 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
     // with lists the host knows the runs: every unit may be whole
     const bool joins = !k || p.blocks % p.pairs != 0 || (p.blocks / p.pairs) % p.list_blocks != 0;
     if (st != IC_OK || !joins) return st;
-    if (launch_ex(tree_join_kernel, dim3((unsigned)all_units, 16), dim3(256), 0, s, pdl, 0, a, p.pairs) != cudaSuccess)
+    // few runs: one piece a warp, for the latency of many runs of one unit; else
+    // four, for fewer warps
+    const bool few = p.pairs <= 32;
+    auto join = few ? tree_join_kernel<1> : tree_join_kernel<4>;
+    if (launch_ex(join, dim3((unsigned)p.pairs, few ? 64 : 16), dim3(256), 0, s, pdl, 0, a) != cudaSuccess)
         return cuda_error("tree_join");
     count_launch(IC_LK_COMBINE);
     return last_launch_status();

@@ -13,11 +13,11 @@
 //     cache keeps as bfloat16 follow in the same accumulator: both operands
 //     carry the same scales there.
 //   P V: the weights w_s = p_s g_s go in as an e4m3 number and an e5m2 number
-//     for the rest: 7 significant bits down to 2^-10 of the row's largest
-//     weight, 3 down to 2^-18, so that many small weights beside a large one
+//     for the rest: 7 significant bits down to 2^-8 of the row's largest
+//     weight, 3 down to 2^-16, so that many small weights beside a large one
 //     are not lost.  The running maximum is that of log2 w_s, which keeps w
 //     in 8-bit range whatever the scales are; the largest weight stands
-//     between 2^4 and 2^8.  The softmax sum adds w_s / g_s in float32.
+//     between 2^2 and 2^8.5.  The softmax sum adds w_s / g_s in float32.
 // Two 8-bit products cost what one of bfloat16 does, without the decoding and
 // with 644 bytes of cache traffic per row.
 //
@@ -91,7 +91,7 @@ constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 384, TM_QR = TM_Q + 96;   // TM_
 constexpr int TMEM_COLS = 512;
 constexpr int MAX_PAIRS = 74;                 // CTA pairs of 148 SMs
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr float TOP = 4.f, SLACK = 4.f;       // log2 of the largest weight when the maximum is
+constexpr float TOP = 2.f, SLACK = 6.5f;       // log2 of the largest weight when the maximum is
                                               // set, and how far it may grow before O is rescaled
 
 struct __align__(8) Bars {
@@ -368,10 +368,15 @@ __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t
         rest = row < rows ? __ldg(reinterpret_cast<const uint4*>(q + row * KVW + DV) + (lane & 7)) : make_uint4(0u, 0u, 0u, 0u);
     }
     if (j > 0) wait_for(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, a.status, &s.abort, 8);
-#pragma unroll
+#pragma unroll 1                        // little code: it runs once per unit, from a cold instruction cache
     for (int i = 0; i < 4; ++i) {
         const int row = warp * 4 + i;
-        const uint32_t u[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+        const uint32_t u[8] = {v[0][0].x, v[0][0].y, v[0][0].z, v[0][0].w, v[0][1].x, v[0][1].y, v[0][1].z, v[0][1].w};
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            v[k][0] = v[k + 1][0];
+            v[k][1] = v[k + 1][1];
+        }
         uint32_t m = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) m = max(m, max(u[k] & 0x7fff0000u, (u[k] << 16) & 0x7fff0000u));

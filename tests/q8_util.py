@@ -11,15 +11,15 @@ Tolerance of the attention, elementwise, for a row with softmax weights p_s
                                   is kept as an e4m3 number and an e5m2 number
                                   for the rest: half a step is 2^-4 of a
                                   number and 2^-3 of the rest, 2^-7 in all.
-                                  The largest weight stands at 2^4 or more.
+                                  The largest weight stands at 2^2 or more.
                                   Weights below e4m3's normal range (2^-6)
                                   leave at most half its smallest step, 2^-10,
-                                  to the rest, an error of 2^-13, 2^-17 of the
+                                  to the rest, an error of 2^-13, 2^-15 of the
                                   largest weight; those below 2^-10 are the
                                   rest alone, off by 2^-3 of themselves, or by
-                                  half of e5m2's smallest step, 2^-17, 2^-21
+                                  half of e5m2's smallest step, 2^-17, 2^-19
                                   of the largest: err_s = max(2^-7 w,
-                                  min(2^-17 max w, 2^-3 w), 2^-21 max w)
+                                  min(2^-15 max w, 2^-3 w), 2^-19 max w)
   + 2 d (sum_s p_s |V_s|)           the logits' error d (natural units):
                                     float32 sums of 576 products, each
                                     rounding 2^-24, in units of the sum of
@@ -135,7 +135,7 @@ def attend(q, kv, scales, seen, scale):
     v = np.abs(k[:, :VALUES])
     w = p * g
     top = w.max(axis=1, keepdims=True)
-    err = np.maximum(np.maximum(2.0 ** -7 * w, np.minimum(2.0 ** -17 * top, 2.0 ** -3 * w)), 2.0 ** -21 * top)
+    err = np.maximum(np.maximum(2.0 ** -7 * w, np.minimum(2.0 ** -15 * top, 2.0 ** -3 * w)), 2.0 ** -19 * top)
     terms = np.abs(q) @ np.abs(k).T * abs(scale)
     floor = np.abs(q).max(axis=1, keepdims=True) * np.abs(k).sum(axis=1) * abs(scale)
     d = (576 * 2.0 ** -24 * terms + 2.0 ** -17 * floor + 2.0 ** -21 * np.abs(s) + 2.0 ** -21).max(axis=1)

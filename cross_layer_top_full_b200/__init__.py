@@ -441,12 +441,36 @@ def _refuse(x, name: str, dtypes, shape, device: int) -> None:
                      % (name, tuple(x.stride())))
 
 
-# These calls are short (a few microseconds on the device), so each check is
-# one comparison and the reasons are worked out only on the way to an error.
-def _dense(x, name: str, dtypes, shape, device: int) -> int:
-    """Address of a contiguous CUDA tensor of the given shape."""
-    if x.get_device() != device or x.dtype not in dtypes or x.shape != shape or not x.is_contiguous():
-        _refuse(x, name, dtypes, shape, device)
+class _Torch:
+    """What the calls below ask of torch, looked up once (this module imports
+    without it).  They take a few microseconds on the device, so on the way to
+    a launch every check is one comparison; _refuse works out the reasons."""
+
+    def __init__(self):
+        import torch
+        self.u8, self.i32, self.i64, self.f32, self.bf16 = (torch.uint8, torch.int32, torch.int64, torch.float32,
+                                                            torch.bfloat16)
+        self.codes = (torch.uint8, torch.float8_e4m3fn)
+        self.cuda = torch.cuda
+        # the current stream's handle without a Stream object around it
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+_torch: Optional[_Torch] = None
+
+
+def _torch_names() -> _Torch:
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
+def _dense(x, name: str, dtype, shape, device: int) -> int:
+    """Address of a contiguous CUDA tensor of the given type and shape."""
+    if x.get_device() != device or x.dtype is not dtype or x.shape != shape or not x.is_contiguous():
+        _refuse(x, name, (dtype,), shape, device)
     return x.data_ptr()
 
 
@@ -454,55 +478,52 @@ def _rows_of(x, name: str, dtypes, width: int, n: int, device: int):
     """Address and row stride of n rows of adjacent values that may lie apart."""
     if x.get_device() != device or x.dtype not in dtypes or x.shape != (n, width):
         _refuse(x, name, dtypes, (n, width), device)
-    if n == 0:
-        return x.data_ptr(), width
     step, unit = x.stride()
-    if unit != 1 or (step < width and n > 1):
+    if n <= 1:                                           # one row or none: the stride means nothing
+        if unit != 1 and n == 1:
+            _refuse(x, name, dtypes, (n, width), device)
+        step = width
+    elif unit != 1 or step < width:
         _refuse(x, name, dtypes, (n, width), device)
-    return x.data_ptr(), step if n > 1 else width        # one row: its stride means nothing
-
-
-def _workspace(ws, device: int):
-    import torch
-    n = ws.shape[0] if ws.dim() == 1 else -1
-    return _dense(ws, "ws", (torch.uint8,), (n,), device), n
-
-
-def _current(device: int, stream) -> Optional[int]:
-    if stream is not None:
-        return _stream(stream)
-    import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    return x.data_ptr(), step
 
 
 def _q8_rows(where, slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale):
     """The checked arguments that writing and reading share: rows and caches
     (address, stride), type, counts, workspace."""
-    import torch
-    device = torch.cuda.current_device()
-    if kv is None and k_idx is None:
-        raise ValueError("%s: give kv, k_idx or both" % where)
-    if (kv is None) != (kv_q8 is None) or (kv is None) != (kv_scale is None):
-        raise ValueError("%s: kv, kv_q8 and kv_scale go together" % where)
-    if (k_idx is None) != (k_codes is None) or (k_idx is None) != (k_scale is None):
+    t = _torch or _torch_names()
+    device = t.cuda.current_device()
+    if kv is None:
+        if k_idx is None:
+            raise ValueError("%s: give kv, k_idx or both" % where)
+        if kv_q8 is not None or kv_scale is not None:
+            raise ValueError("%s: kv, kv_q8 and kv_scale go together" % where)
+        rows, cache = k_idx, k_codes
+    else:
+        if kv_q8 is None or kv_scale is None:
+            raise ValueError("%s: kv, kv_q8 and kv_scale go together" % where)
+        rows, cache = kv, kv_q8
+    if (k_codes is None) != (k_idx is None) or (k_scale is None) != (k_idx is None):
         raise ValueError("%s: k_idx, k_codes and k_scale go together" % where)
-    rows, cache = (k_idx, k_codes) if kv is None else (kv, kv_q8)
     n, num_rows, dtype = rows.shape[0], cache.shape[0], rows.dtype
-    f32 = (torch.float32,)
-    types = (dtype,) if dtype is torch.bfloat16 or dtype is torch.float32 else ()
-    p = kq = ks = q = kc = sc = None
+    types = (dtype,) if dtype is t.bf16 or dtype is t.f32 else ()
+    p = kq = ks = q = kc = sc = at = None
     kv_step, k_step = 576, 128
     if kv is not None:
         p, kv_step = _rows_of(kv, "kv", types, 576, n, device)
-        kq = _dense(kv_q8, "kv_q8", (torch.uint8,), (num_rows, Q8_ROW_BYTES), device)
-        ks = _dense(kv_scale, "kv_scale", f32, (num_rows,), device)
+        kq = _dense(kv_q8, "kv_q8", t.u8, (num_rows, Q8_ROW_BYTES), device)
+        ks = _dense(kv_scale, "kv_scale", t.f32, (num_rows,), device)
     if k_idx is not None:
         q, k_step = _rows_of(k_idx, "k_idx", types, 128, n, device)
-        kc = _dense(k_codes, "k_codes", (torch.uint8, torch.float8_e4m3fn), (num_rows, 128), device)
-        sc = _dense(k_scale, "k_scale", f32, (num_rows,), device)
-    at = None if slots is None else _dense(slots, "slots", (torch.int32,), (n,), device)
-    w, w_bytes = _workspace(ws, device)
-    return device, p, kv_step, q, k_step, F32 if dtype is torch.float32 else BF16, n, at, kq, ks, kc, sc, num_rows, w, w_bytes
+        if k_codes.dtype not in t.codes:
+            _refuse(k_codes, "k_codes", t.codes, (num_rows, 128), device)
+        kc = _dense(k_codes, "k_codes", k_codes.dtype, (num_rows, 128), device)
+        sc = _dense(k_scale, "k_scale", t.f32, (num_rows,), device)
+    if slots is not None:
+        at = _dense(slots, "slots", t.i32, (n,), device)
+    w_bytes = ws.numel()
+    w = _dense(ws, "ws", t.u8, (w_bytes,), device)
+    return device, p, kv_step, q, k_step, F32 if dtype is t.f32 else BF16, n, at, kq, ks, kc, sc, num_rows, w, w_bytes
 
 
 def cache_write_q8(slots, ws, *, kv=None, kv_q8=None, kv_scale=None, k_idx=None, k_codes=None,
@@ -515,7 +536,8 @@ def cache_write_q8(slots, ws, *, kv=None, kv_q8=None, kv_scale=None, k_idx=None,
     device, kv, kvs, ki, kis, dt, n, at, kq, ks, kc, sc, num_rows, w, wb = _q8_rows(
         "cache_write_q8", slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale)
     _check(lib().ic_cache_write_q8(kv, kvs, ki, kis, dt, n, at, kq, ks, kc, sc, num_rows, w, wb,
-                                   _current(device, stream)), "ic_cache_write_q8")
+                                   _torch.raw_stream(device) if stream is None else _stream(stream)),
+           "ic_cache_write_q8")
 
 
 def cache_read_q8(slots, ws, *, kv=None, kv_q8=None, kv_scale=None, k_idx=None, k_codes=None,
@@ -525,7 +547,8 @@ def cache_read_q8(slots, ws, *, kv=None, kv_q8=None, kv_scale=None, k_idx=None, 
     device, kv, kvs, ki, kis, dt, n, at, kq, ks, kc, sc, num_rows, w, wb = _q8_rows(
         "cache_read_q8", slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale)
     _check(lib().ic_cache_read_q8(kq, ks, kc, sc, num_rows, n, at, dt, kv, kvs, ki, kis, w, wb,
-                                  _current(device, stream)), "ic_cache_read_q8")
+                                  _torch.raw_stream(device) if stream is None else _stream(stream)),
+           "ic_cache_read_q8")
 
 
 def tree_attn_q8_workspace_size(pr: PagedRows, k: int, Hq: int) -> int:
@@ -539,19 +562,19 @@ def tree_attn_q8_paged(q, kv_q8, kv_scale, idx, pr: PagedRows, scale: float, out
     a sequence are the nodes of a tree of drafted tokens.  tree [B, Lq] int64:
     bit a of a row is set when it sees node a (None: a chain).  idx [B, Lq, k]
     int32 restricts a row to the positions it names (None: every position)."""
-    import torch
-    device = torch.cuda.current_device()
+    t = _torch or _torch_names()
+    device = t.cuda.current_device()
     B, Lq, rows = pr.B, pr.Lq, pr.num_pages * pr.page_size
     Hq, k = q.shape[-2] if q.dim() == 4 else 0, 0 if idx is None else idx.shape[-1]
     if idx is not None and k == 0:
         raise ValueError("idx: names no position; None stands for every position")
-    bf16 = (torch.bfloat16,)
-    w, w_bytes = _workspace(ws, device)
+    w_bytes = ws.numel()
     _check(lib().ic_tree_attn_q8_paged(
-        _dense(q, "q", bf16, (B, Lq, Hq, 576), device),
-        _dense(kv_q8, "kv_q8", (torch.uint8,), (rows, Q8_ROW_BYTES), device),
-        _dense(kv_scale, "kv_scale", (torch.float32,), (rows,), device),
-        None if idx is None else _dense(idx, "idx", (torch.int32,), (B, Lq, k), device), k,
-        None if tree is None else _dense(tree, "tree", (torch.int64,), (B, Lq), device),
-        ctypes.byref(pr), Hq, float(scale), _dense(out, "out", bf16, (B, Lq, Hq, 512), device),
-        w, w_bytes, _current(device, stream)), "ic_tree_attn_q8_paged")
+        _dense(q, "q", t.bf16, (B, Lq, Hq, 576), device),
+        _dense(kv_q8, "kv_q8", t.u8, (rows, Q8_ROW_BYTES), device),
+        _dense(kv_scale, "kv_scale", t.f32, (rows,), device),
+        None if idx is None else _dense(idx, "idx", t.i32, (B, Lq, k), device), k,
+        None if tree is None else _dense(tree, "tree", t.i64, (B, Lq), device),
+        ctypes.byref(pr), Hq, float(scale), _dense(out, "out", t.bf16, (B, Lq, Hq, 512), device),
+        _dense(ws, "ws", t.u8, (w_bytes,), device), w_bytes,
+        t.raw_stream(device) if stream is None else _stream(stream)), "ic_tree_attn_q8_paged")

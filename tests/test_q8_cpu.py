@@ -155,6 +155,12 @@ class _Dev:
     def get_device(self):
         return self.device.index if self.is_cuda else -1
 
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
     def dim(self):
         return len(self.shape)
 

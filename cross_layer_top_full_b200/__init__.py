@@ -455,6 +455,16 @@ class _Torch:
         # the current stream's handle without a Stream object around it
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                   lambda device: torch.cuda.current_stream(device).cuda_stream)
+        # The same checks in C++ (csrc/fastcall.cpp), for plain tensors only;
+        # without it, or where it declines, the calls below make them here.
+        self.tensor, self.fast = torch.Tensor, None
+        try:
+            from . import _fastcall
+        except ImportError:
+            return
+        _fastcall.bind(*(ctypes.cast(f, _P).value for f in (
+            lib().ic_cache_write_q8, lib().ic_cache_read_q8, lib().ic_tree_attn_q8_paged)))
+        self.fast = _fastcall
 
 
 _torch: Optional[_Torch] = None
@@ -533,6 +543,13 @@ def cache_write_q8(slots, ws, *, kv=None, kv_q8=None, kv_scale=None, k_idx=None,
     the caches kv_q8 [num_rows, 640] uint8 with kv_scale [num_rows], k_codes
     [num_rows, 128] with k_scale [num_rows].  -1 skips a row; slots None: row
     n is cache row n.  No two rows may name the same slot."""
+    t = _torch or _torch_names()
+    if t.fast is not None and type(ws) is t.tensor:
+        device = t.cuda.current_device()
+        code = t.fast.cache_write_q8(slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale, device,
+                                     t.raw_stream(device) if stream is None else _stream(stream) or 0)
+        if code is not None:
+            return _check(code, "ic_cache_write_q8") if code else None
     device, kv, kvs, ki, kis, dt, n, at, kq, ks, kc, sc, num_rows, w, wb = _q8_rows(
         "cache_write_q8", slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale)
     _check(lib().ic_cache_write_q8(kv, kvs, ki, kis, dt, n, at, kq, ks, kc, sc, num_rows, w, wb,
@@ -544,6 +561,13 @@ def cache_read_q8(slots, ws, *, kv=None, kv_q8=None, kv_scale=None, k_idx=None, 
                   k_scale=None, stream=None) -> None:
     """The reverse of cache_write_q8: rows slots[n] of the caches into kv
     [n, 576] and/or k_idx [n, 128]; -1 gives a row of zeros."""
+    t = _torch or _torch_names()
+    if t.fast is not None and type(ws) is t.tensor:
+        device = t.cuda.current_device()
+        code = t.fast.cache_read_q8(slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale, device,
+                                    t.raw_stream(device) if stream is None else _stream(stream) or 0)
+        if code is not None:
+            return _check(code, "ic_cache_read_q8") if code else None
     device, kv, kvs, ki, kis, dt, n, at, kq, ks, kc, sc, num_rows, w, wb = _q8_rows(
         "cache_read_q8", slots, ws, kv, kv_q8, kv_scale, k_idx, k_codes, k_scale)
     _check(lib().ic_cache_read_q8(kq, ks, kc, sc, num_rows, n, at, dt, kv, kvs, ki, kis, w, wb,
@@ -564,6 +588,11 @@ def tree_attn_q8_paged(q, kv_q8, kv_scale, idx, pr: PagedRows, scale: float, out
     int32 restricts a row to the positions it names (None: every position)."""
     t = _torch or _torch_names()
     device = t.cuda.current_device()
+    if t.fast is not None and type(ws) is t.tensor:
+        code = t.fast.tree_attn_q8(q, kv_q8, kv_scale, idx, tree, pr, scale, out, ws, device,
+                                   t.raw_stream(device) if stream is None else _stream(stream) or 0)
+        if code is not None:
+            return _check(code, "ic_tree_attn_q8_paged") if code else None
     B, Lq, rows = pr.B, pr.Lq, pr.num_pages * pr.page_size
     Hq, k = q.shape[-2] if q.dim() == 4 else 0, 0 if idx is None else idx.shape[-1]
     if idx is not None and k == 0:

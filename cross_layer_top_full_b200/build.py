@@ -3,16 +3,19 @@
 ``python -m cross_layer_top_full_b200.build`` (or ``build()``) compiles every
 ``csrc/*.cu`` with nvcc for ``sm_100a`` and links ``libindexcache.so`` next to
 this file.  Objects go to ``_build/`` and are rebuilt only when a source or
-header is newer.
+header is newer.  Where torch is installed, ``csrc/fastcall.cpp`` becomes
+``_fastcall.so``: the short way of the quantised-cache calls from Python.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libindexcache.so")
+FAST = os.path.join(PKG, "_fastcall.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -56,6 +60,25 @@ def _compile(nvcc: str, src: str, verbose: bool, ptxas_v: bool) -> str:
     return obj
 
 
+def _build_fastcall(verbose: bool) -> None:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return
+    src, header = os.path.join(CSRC, "fastcall.cpp"), os.path.join(INCLUDE, "indexcache.h")
+    if os.path.exists(FAST) and os.path.getmtime(FAST) >= max(os.path.getmtime(src), os.path.getmtime(header)):
+        return
+    torch = os.path.dirname(spec.origin)
+    libs = os.path.join(torch, "lib")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           "-I", INCLUDE, "-I", os.path.join(torch, "include"),
+           "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], src, "-o", FAST,
+           "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + libs]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+
+
 def build(verbose: bool = False, ptxas_v: bool = False) -> str:
     """Compile and link the library; returns the path of the .so."""
     os.makedirs(OBJDIR, exist_ok=True)
@@ -68,6 +91,7 @@ def build(verbose: bool = False, ptxas_v: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
+    _build_fastcall(verbose)
     return LIB
 
 

@@ -523,6 +523,46 @@ def test_a_full_gpu_of_rows(dev):
     np.testing.assert_allclose(num(alone[0]), num(out[39]), rtol=2.0 ** -6, atol=2.0 ** -8)
 
 
+# ---------------------------------------------------------------- refusals
+def test_calls_refuse_wrong_tensors(dev):
+    """Real tensors take the short way through the binding; what is wrong with one is said all the same."""
+    kv, c, ws = torch.zeros(4, 576, dtype=BF, device=dev), caches(8, dev), make_ws(0, dev)
+    slots = torch.arange(4, dtype=torch.int32, device=dev)
+    good = dict(kv=kv, kv_q8=c["kv_q8"], kv_scale=c["kv_scale"])
+    n0 = ic.kernel_launches(0)
+    for bad, match in ((dict(kv=kv.half()), "kv: unexpected dtype"), (dict(kv=kv.cpu()), "kv: expected a tensor on"),
+                       (dict(kv=kv.t().contiguous().t()), "kv: expected a contiguous"),
+                       (dict(kv=kv[:1].expand(4, 576)), "kv: expected a contiguous"),
+                       (dict(kv_q8=c["kv_q8"][:, :512]), "kv_q8: expected shape"),
+                       (dict(kv_q8=torch.zeros(8, 1280, dtype=torch.uint8, device=dev)[:, :640]), "kv_q8: expected a contiguous"),
+                       (dict(kv_scale=c["kv_scale"].double()), "kv_scale: unexpected dtype"),
+                       (dict(kv_scale=None), "go together"), (dict(k_codes=c["k_codes"]), "go together")):
+        for call in (ic.cache_write_q8, ic.cache_read_q8):
+            with pytest.raises(ValueError, match=match):
+                call(slots, ws, **{**good, **bad})
+    with pytest.raises(ValueError, match="slots: unexpected dtype"):
+        ic.cache_write_q8(slots.long(), ws, **good)
+    with pytest.raises(ic.IcError):
+        ic.cache_write_q8(None, ws, kv=torch.zeros(9, 576, dtype=BF, device=dev), kv_q8=c["kv_q8"], kv_scale=c["kv_scale"])
+    with pytest.raises(ic.IcError):
+        ic.cache_write_q8(slots, ws[:128], **good)
+    b = Tree([50], 2, dev, seed=41, Hq=4)
+    b.device()
+    out, aws = torch.empty(1, 2, 4, 512, dtype=BF, device=dev), b.workspace()
+    for name, x, match in (("d_q", b.d_q.float(), "q: unexpected dtype"), ("d_cache", b.d_cache[1:], "kv_q8: expected shape"),
+                           ("d_scale", b.d_scale[::2].repeat(2)[1:], "kv_scale: expected shape"),
+                           ("d_tree", b.d_tree.int(), "tree: unexpected dtype"),
+                           ("d_q", b.d_q.transpose(1, 2).contiguous().transpose(1, 2), "q: expected a contiguous")):
+        keep = getattr(b, name)
+        setattr(b, name, x)
+        with pytest.raises(ValueError, match=match):
+            b.call(out, aws)
+        setattr(b, name, keep)
+    with pytest.raises(ic.IcError):
+        b.call(out, aws[:512])
+    assert ic.kernel_launches(0) == n0 and ic.read_status(ws) == 0
+
+
 # ---------------------------------------------------------------- together
 def test_a_serving_step_from_write_to_attention(dev):
     """A prompt and then a tree of drafted tokens are written into the pages,

@@ -246,3 +246,23 @@ def test_binding_checks_tree_attention_tensors(lib, device0):
     refused("out: expected shape", out=_Dev(2, 3, 15, 512, dtype=bf))
     refused("ws: expected a tensor on cuda:0", ws=_Dev(1 << 20, cuda=False))
     assert ic.kernel_launches(0) == before
+
+
+def test_the_short_way_declines_what_is_not_plainly_right(lib):
+    """csrc/fastcall.cpp makes a call only of plain CUDA tensors; anything else goes the long way."""
+    fast = ic._torch_names().fast
+    assert fast is not None, "build _fastcall.so: python -m cross_layer_top_full_b200.build"
+    before = ic.kernel_launches(0)
+    cpu, dev = torch.zeros(4, 576, dtype=torch.bfloat16), _Dev(4, 576, dtype=torch.bfloat16)
+    for kv in (None, cpu, dev, "kv", cpu.numpy):
+        for call in (fast.cache_write_q8, fast.cache_read_q8):
+            assert call(None, torch.zeros(256, dtype=torch.uint8), kv, kv, kv, None, None, None, 0, 0) is None
+    assert fast.cache_write_q8(None, None) is None                # a wrong number of arguments
+    pr = ic.PagedRows(1, 1, 8, 4096, 4096, 1, 128, 1)
+    for x in (None, cpu, dev):
+        assert fast.tree_attn_q8(x, x, x, None, None, pr, 0.1, x, x, 0, 0) is None
+        assert fast.tree_attn_q8(x, x, x, None, None, b"short", 0.1, x, x, 0, 0) is None
+        assert fast.tree_attn_q8(x, x, x, None, None, pr, "scale", x, x, 0, 0) is None
+    with pytest.raises(TypeError):
+        fast.bind(1)
+    assert ic.kernel_launches(0) == before

@@ -971,9 +971,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
 // ------------------------------------------------------------------ joining partial results
 // out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the runs that share
 // a unit; blockIdx.x is the run in which the unit ends.  A warp takes 32 rows
-// of N 16-byte pieces (neighbours in a chunk of one writing warp), with four
-// runs' loads in flight.
-template <int N>
+// of N 16-byte pieces (neighbours in a chunk of one writing warp).  The runs
+// are read CH at a time, maxima, sums and pieces at once (one memory round trip
+// per chunk); the running maximum rescales what earlier chunks added.
+template <int N, int CH>
 __global__ void __launch_bounds__(256)
 tree_join_kernel(const __grid_constant__ Args a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -985,26 +986,41 @@ tree_join_kernel(const __grid_constant__ Args a) {
     const int at = piece % (8 / N) * N, c = piece / (8 / N) & 1, owner = piece / (16 / N) & 15, rank = piece / (256 / N);
     const int m = rank * HROWS + (owner & 1) * 32 + lane;
     if (m >= join.z) return;
-    // slot of a run: 1 where the unit begins in it, 0 where it continues the unit
-    float top = -INFINITY;
-#pragma unroll 4
-    for (int p = p0; p <= p1; ++p) top = fmaxf(top, __ldg(&a.part_ml[(2 * p + (p == p0)) * MROWS + m].x));
+    float top = -INFINITY, l = 0.f;
     float4 o[N];
-    float l = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int p = p0; p <= p1; ++p) {
-        const int slot = 2 * p + (p == p0);
-        const float2 ml = __ldg(a.part_ml + slot * MROWS + m);
-        // a run that saw nothing of the row has weight 0 (its sum is 0, or a NaN that stays)
-        const float wgt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_approx(ml.x - top);
-        l += wgt * ml.y;
+    for (int p = p0; p <= p1; p += CH) {
+        float2 ml[CH];
+        uint4 v[CH][N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint4 v = __ldg(a.part_o + part_at(slot, rank, owner, c, at + i, lane));
-            o[i].x += wgt * __uint_as_float(v.x); o[i].y += wgt * __uint_as_float(v.y);
-            o[i].z += wgt * __uint_as_float(v.z); o[i].w += wgt * __uint_as_float(v.w);
+        for (int c2 = 0; c2 < CH; ++c2) {
+            // slot of a run: 1 where the unit begins in it, 0 where it continues the unit
+            const bool there = p + c2 <= p1;
+            const int slot = 2 * (p + c2) + (p + c2 == p0);
+            ml[c2] = there ? __ldg(a.part_ml + slot * MROWS + m) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[c2][i] = there ? __ldg(a.part_o + part_at(slot, rank, owner, c, at + i, lane)) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        float mc = top;
+#pragma unroll
+        for (int c2 = 0; c2 < CH; ++c2) mc = fmaxf(mc, ml[c2].x);
+        const float scale = top == mc ? 1.f : ex2_approx(top - mc);
+        l *= scale;
+#pragma unroll
+        for (int i = 0; i < N; ++i) { o[i].x *= scale; o[i].y *= scale; o[i].z *= scale; o[i].w *= scale; }
+        top = mc;
+#pragma unroll
+        for (int c2 = 0; c2 < CH; ++c2) {
+            // a run that saw nothing of the row has weight 0 (its sum is 0, or a NaN that stays)
+            const float wgt = ml[c2].x == -INFINITY ? (ml[c2].y == 0.f ? 0.f : 1.f) : ex2_approx(ml[c2].x - top);
+            l += wgt * ml[c2].y;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                o[i].x += wgt * __uint_as_float(v[c2][i].x); o[i].y += wgt * __uint_as_float(v[c2][i].y);
+                o[i].z += wgt * __uint_as_float(v[c2][i].z); o[i].w += wgt * __uint_as_float(v[c2][i].w);
+            }
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1104,7 +1120,7 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
     // few runs: one piece a warp, for the latency of many runs of one unit; else
     // four, for fewer warps
     const bool few = p.pairs <= 32;
-    auto join = few ? tree_join_kernel<1> : tree_join_kernel<4>;
+    auto join = few ? tree_join_kernel<1, 8> : tree_join_kernel<4, 2>;
     if (launch_ex(join, dim3((unsigned)p.pairs, few ? 64 : 16), dim3(256), 0, s, pdl, 0, a) != cudaSuccess)
         return cuda_error("tree_join");
     count_launch(IC_LK_COMBINE);

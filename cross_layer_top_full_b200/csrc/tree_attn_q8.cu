@@ -144,11 +144,23 @@ __device__ __forceinline__ int blocks_of(const Args& a, int b) {
 __device__ __forceinline__ int total_blocks(const Args& a) {
     if (a.idx) return a.B * a.units * a.list_blocks;
     int n = 0;
+#pragma unroll 8
     for (int b = threadIdx.x & 31; b < a.B; b += 32) n += blocks_of(a, b);
     return __reduce_add_sync(0xffffffffu, n) * a.units;
 }
 
-// Runs of the pairs: n blocks over P pairs, the first n % P one block longer.
+// How the blocks are shared out.  A unit costs a run about UNIT_COST blocks
+// (measured: 12,000 to 14,000 cycles for Q, the first block's latency and the
+// results, against 3,600 a block), so with few units a pair takes a part of
+// one only: units of sequence b get parts_of(b) pairs each, in proportion to
+// their blocks.  Otherwise, or where that would leave a pair with more blocks
+// than the second unit costs it, the list is cut into equal runs.  32 lists of
+// 2048: 64 pairs of 8 blocks, 25 us, against 74 runs of 7 over up to two units,
+// 33 us.
+constexpr int UNIT_COST = 3;
+__device__ __forceinline__ int parts_of(const Args& a, int b, int n, int P) { return max(1, blocks_of(a, b) * P / n); }
+
+// Equal runs: n blocks over P pairs, the first n % P one block longer.
 __device__ __forceinline__ int pairs_of(int n, int max_pairs) { return min(n, max_pairs); }
 __device__ __forceinline__ int run_begin(int n, int P, int p) { return n / P * p + min(n % P, p); }
 __device__ __forceinline__ int pair_with(int n, int P, int t) {
@@ -286,15 +298,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// Two query values (a bfloat16 pair) divided by their row's scale, as e4m3
-// numbers and e4m3 numbers for what they leave.  By way of float16, which holds
-// a bfloat16 in [-448, 448] down to 2^-24 exactly, as it does the rest.
-__device__ __forceinline__ void split_query(uint32_t p, float inv, uint32_t& hi, uint32_t& lo) {
-    const __half2 h = __floats2half2_rn(__uint_as_float(p << 16) * inv, __uint_as_float(p & 0xffff0000u) * inv);
+// Two scaled query values (a bfloat16 pair) as e4m3 numbers and e4m3 numbers
+// for what they leave.  By way of float16, which holds a bfloat16 in [-448,
+// 448] down to 2^-24 exactly, as it does the rest.
+__device__ __forceinline__ void split_query(uint32_t p, uint32_t& hi, uint32_t& lo) {
+    const __half2 h = __floats2half2_rn(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
     hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
     const __half2 d = __hsub2(h, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
     lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(d), __NV_SATFINITE, __NV_E4M3);
 }
+// A bfloat16 pair times a power of two (a bfloat16 pair of it): exact.
+__device__ __forceinline__ uint32_t mul_pair(uint32_t p, uint32_t pow2) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(p), "r"(pow2));
+    return r;
+}
+__device__ __forceinline__ uint32_t twice(float pow2) { return (__float_as_uint(pow2) >> 16) * 0x10001u; }
 
 // Bits of the 32 positions from s0 on that a row sees by its tree mask.
 __device__ __forceinline__ uint32_t tree_bits(unsigned long long mask, int off) {   // off = s0 - ctx
@@ -369,45 +388,41 @@ __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t
     }
     if (j > 0) wait_for(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, a.status, &s.abort, 8);
 #pragma unroll 1                        // little code: it runs once per unit, from a cold instruction cache
-    for (int i = 0; i < 4; ++i) {
-        const int row = warp * 4 + i;
-        const uint32_t u[8] = {v[0][0].x, v[0][0].y, v[0][0].z, v[0][0].w, v[0][1].x, v[0][1].y, v[0][1].z, v[0][1].w};
+    for (int i0 = 0; i0 < 4; i0 += 2) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            v[k][0] = v[k + 1][0];
-            v[k][1] = v[k + 1][1];
+        for (int i = 0; i < 2; ++i) {
+            const int row = warp * 4 + i0 + i;
+            const uint32_t u[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+            uint32_t m = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m = __vmaxu2(m, u[k] & 0x7fff7fffu);
+            m = __reduce_max_sync(0xffffffffu, max(m << 16, m & 0xffff0000u));
+            const bool finite = m < 0x7f800000u;
+            const int e = finite ? scale_exponent(m) : 0;
+            const uint32_t inv = finite ? twice(exp2_int(-e)) : 0x7fff7fffu;
+            if (lane == 0) sq[row] = exp2_int(e);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t h0, l0, h1, l1;
+                split_query(mul_pair(u[2 * k], inv), h0, l0);
+                split_query(mul_pair(u[2 * k + 1], inv), h1, l1);
+                hi[k] = h0 | h1 << 16;
+                lo[k] = l0 | l1 << 16;
+            }
+            const int at = row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4*>(smem + OFF_Q + (lane >> 3) * ATOM + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(smem + (lane < 8 ? OFF_Q + 4 * ATOM : OFF_P + ((lane >> 3) - 1) * ATOM) + at) =
+                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            v[i][0] = v[i + 2][0];
+            v[i][1] = v[i + 2][1];
         }
-        uint32_t m = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m = max(m, max(u[k] & 0x7fff0000u, (u[k] << 16) & 0x7fff0000u));
-        m = __reduce_max_sync(0xffffffffu, m);
-        const bool finite = m < 0x7f800000u;
-        const int e = finite ? scale_exponent(m) : 0;
-        const float inv = finite ? exp2_int(-e) : __uint_as_float(0x7fffffffu);
-        if (lane == 0) sq[row] = exp2_int(e);
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t h0, l0, h1, l1;
-            split_query(u[2 * k], inv, h0, l0);
-            split_query(u[2 * k + 1], inv, h1, l1);
-            hi[k] = h0 | h1 << 16;
-            lo[k] = l0 | l1 << 16;
-        }
-        const int at = row * 128 + (((lane & 7) ^ (row & 7)) << 4);
-        *reinterpret_cast<uint4*>(smem + OFF_Q + (lane >> 3) * ATOM + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(smem + (lane < 8 ? OFF_Q + 4 * ATOM : OFF_P + ((lane >> 3) - 1) * ATOM) + at) =
-            make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     __syncwarp();
     {
         const int row = warp * 4 + (lane >> 3);
-        const float inv = 1.f / sq[row];
-        const uint32_t u[4] = {rest.x, rest.y, rest.z, rest.w};
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            w[k] = bf16_pair(__uint_as_float(u[k] << 16) * inv, __uint_as_float(u[k] & 0xffff0000u) * inv);
+        const uint32_t inv = twice(__uint_as_float(0x7f000000u - __float_as_uint(sq[row])));     // 1 / 2^n
+        const uint32_t w[4] = {mul_pair(rest.x, inv), mul_pair(rest.y, inv), mul_pair(rest.z, inv), mul_pair(rest.w, inv)};
         *reinterpret_cast<uint4*>(smem + OFF_P + 3 * ATOM + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
             make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -467,44 +482,77 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
     pdl_wait();
     if (warp == W_RES) {             // this pair's run
         const int n = total_blocks(a), P = pairs_of(n, gridDim.x / 2), p = blockIdx.x / 2;
-        int begin = 0, left = 0;
-        if (p < P) {
-            begin = run_begin(n, P, p);
+        bool parts = a.B * a.units <= P;
+        if (parts && a.idx) {        // units of one length: no sums over the sequences
+            const int k = parts_of(a, 0, n, P);
+            parts = a.B * a.units * k <= P && (a.list_blocks + k - 1) / k <= (n + P - 1) / P + UNIT_COST;
+        } else if (parts) {
+            int used = 0, longest = 0;
+            for (int i = lane; i < a.B; i += 32) {
+                const int k = parts_of(a, i, n, P);
+                used += k;
+                longest = max(longest, (blocks_of(a, i) + k - 1) / k);
+            }
+            used = __reduce_add_sync(0xffffffffu, used) * a.units;
+            longest = __reduce_max_sync(0xffffffffu, longest);
+            parts = used <= P && longest <= (n + P - 1) / P + UNIT_COST;
+        }
+        // this pair's place in the list of parts, or its first block in the list of blocks
+        int off = parts ? p : 0, left = 0, begin = 0;
+        if (!parts && p < P) {
+            off = begin = run_begin(n, P, p);
             left = run_begin(n, P, p + 1) - begin;
         }
-        int b = 0, off = begin;      // off: blocks between sequence b's first and the run's first
+        int b = a.B;                 // the sequence that off lies in (a.B: none), off then counts from its first
         if (a.idx) {
-            b = begin / (a.units * a.list_blocks);
-            off = begin % (a.units * a.list_blocks);
-        } else if (left > 0) {
-            for (int b0 = 0; b0 < a.B; b0 += 32) {
-                const int c = b0 + lane < a.B ? blocks_of(a, b0 + lane) * a.units : 0;
+            const int per = a.units * (parts ? parts_of(a, 0, n, P) : a.list_blocks);
+            b = parts || left > 0 ? min(off / per, a.B) : a.B;
+            off %= per;
+        } else if (parts || left > 0) {
+            for (int b0 = 0; b0 < a.B && b == a.B; b0 += 32) {
+                const int at = b0 + lane;
+                const int c = at >= a.B ? 0 : (parts ? parts_of(a, at, n, P) : blocks_of(a, at)) * a.units;
+                const int sum = __reduce_add_sync(0xffffffffu, c);
+                if (off >= sum) {
+                    off -= sum;
+                    continue;
+                }
                 int x = c;           // inclusive prefix sum
                 for (int o = 1; o < 32; o <<= 1) {
                     const int y = __shfl_up_sync(0xffffffffu, x, o);
                     if (lane >= o) x += y;
                 }
-                const unsigned hit = __ballot_sync(0xffffffffu, off < x);
-                if (hit) {
-                    const int l = __ffs(hit) - 1;
-                    b = b0 + l;
-                    off -= __shfl_sync(0xffffffffu, x - c, l);
-                    break;
-                }
-                off -= __shfl_sync(0xffffffffu, x, 31);
+                const int l = __ffs(__ballot_sync(0xffffffffu, off < x)) - 1;
+                b = b0 + l;
+                off -= __shfl_sync(0xffffffffu, x - c, l);
             }
         }
         if (lane == 0) {
-            const int nt = left > 0 ? blocks_of(a, b) : 1, t = off % nt;
-            s.start_b = b;
-            s.start_u = off / nt;
+            int u = 0, t = 0, from = 0;
+            bool ends = false;       // the unit that the run begins inside ends in it; `from`: its first pair
+            if (b < a.B) {
+                const int nt = blocks_of(a, b);
+                if (parts) {
+                    const int k = parts_of(a, b, n, P), i = off % k;
+                    u = off / k;
+                    t = run_begin(nt, k, i);
+                    left = run_begin(nt, k, i + 1) - t;
+                    ends = k > 1 && i == k - 1;
+                    from = p - i;
+                } else {
+                    u = off / nt;
+                    t = off % nt;
+                    ends = t > 0 && left >= nt - t;
+                    if (ends) from = pair_with(n, P, begin - t);
+                }
+            }
+            s.start_b = min(b, a.B - 1);
+            s.start_u = u;
             s.start_t = t;
             s.left = left;
             if (rank == 0) {
-                const Rows r = unit_rows(a, b, off / nt);
-                const bool ends = left > 0 && t > 0 && left >= nt - t;
-                a.joins[p] = make_int4((int)(uint32_t)r.first, (int)(r.first >> 32), ends ? r.rows : 0,
-                                       ends ? pair_with(n, P, begin - t) : 0);
+                const Rows r = unit_rows(a, s.start_b, u);
+                a.joins[p] = make_int4((int)(uint32_t)r.first, (int)(r.first >> 32), ends ? r.rows : 0, from);
             }
         }
     }
@@ -1114,9 +1162,7 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
         return cuda_error("tree_attn_q8");
     count_launch(IC_LK_TREE);
     ic_status st = last_launch_status();
-    // with lists the host knows the runs: every unit may be whole
-    const bool joins = !k || p.blocks % p.pairs != 0 || (p.blocks / p.pairs) % p.list_blocks != 0;
-    if (st != IC_OK || !joins) return st;
+    if (st != IC_OK || p.list_blocks == 1) return st;        // units of one block are always whole
     // few runs: one piece a warp, for the latency of many runs of one unit; else
     // four, for fewer warps
     const bool few = p.pairs <= 32;

@@ -128,6 +128,7 @@ struct Args {
     int k, B, Lq, Hq, T_max, max_pages, page_size, num_pages;
     int units;          // per sequence
     int list_blocks;    // blocks of a list (idx given)
+    int sharing;        // BY_LENGTH without lists
     float scale_log2;
 };
 
@@ -149,15 +150,20 @@ __device__ __forceinline__ int total_blocks(const Args& a) {
     return __reduce_add_sync(0xffffffffu, n) * a.units;
 }
 
-// How the blocks are shared out.  A unit costs a run about UNIT_COST blocks
-// (measured: 12,000 to 14,000 cycles for Q, the first block's latency and the
-// results, against 3,600 a block), so with few units a pair takes a part of
-// one only: units of sequence b get parts_of(b) pairs each, in proportion to
-// their blocks.  Otherwise, or where that would leave a pair with more blocks
-// than the second unit costs it, the list is cut into equal runs.  32 lists of
-// 2048: 64 pairs of 8 blocks, 25 us, against 74 runs of 7 over up to two units,
-// 33 us.
-constexpr int UNIT_COST = 3;
+// How the blocks are shared out among P pairs.  In blocks' time (3,600 cycles)
+// a unit costs a run about UNIT_COST (12,000 to 14,000 cycles for Q, the first
+// block's latency and the results), and joining partial results JOIN_COST (up
+// to 10 us of a second kernel).  Three ways:
+//   WHOLE  the units, whole, in equal shares (nothing to join)
+//   PARTS  each unit over parts_of() pairs, in proportion to its blocks; a pair
+//          has one unit
+//   RUNS   the list of blocks in equal runs, over the units' borders
+// Lists are all of one length: the host takes the cheapest.  With every
+// position the lengths are known on the device, which decides between PARTS
+// and RUNS.  Measured: 32 lists of 2048 (16 blocks), PARTS 25 us, RUNS 33;
+// 128 lists of 2048, WHOLE 137,000 cycles expected, RUNS 134,000 and the join.
+enum { WHOLE, PARTS, RUNS, BY_LENGTH };
+constexpr int UNIT_COST = 3, JOIN_COST = 4;
 __device__ __forceinline__ int parts_of(const Args& a, int b, int n, int P) { return max(1, blocks_of(a, b) * P / n); }
 
 // Equal runs: n blocks over P pairs, the first n % P one block longer.
@@ -482,11 +488,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
     pdl_wait();
     if (warp == W_RES) {             // this pair's run
         const int n = total_blocks(a), P = pairs_of(n, gridDim.x / 2), p = blockIdx.x / 2;
-        bool parts = a.B * a.units <= P;
-        if (parts && a.idx) {        // units of one length: no sums over the sequences
-            const int k = parts_of(a, 0, n, P);
-            parts = a.B * a.units * k <= P && (a.list_blocks + k - 1) / k <= (n + P - 1) / P + UNIT_COST;
-        } else if (parts) {
+        bool parts = a.sharing == PARTS;
+        if (a.sharing == BY_LENGTH && a.B * a.units <= P) {
             int used = 0, longest = 0;
             for (int i = lane; i < a.B; i += 32) {
                 const int k = parts_of(a, i, n, P);
@@ -499,7 +502,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
         }
         // this pair's place in the list of parts, or its first block in the list of blocks
         int off = parts ? p : 0, left = 0, begin = 0;
-        if (!parts && p < P) {
+        if (a.sharing == WHOLE) {
+            const int units = a.B * a.units;
+            if (p < min(units, P)) {
+                off = begin = run_begin(units, min(units, P), p) * a.list_blocks;
+                left = run_begin(units, min(units, P), p + 1) * a.list_blocks - begin;
+            }
+        } else if (!parts && p < P) {
             off = begin = run_begin(n, P, p);
             left = run_begin(n, P, p + 1) - begin;
         }
@@ -1018,64 +1027,70 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
 
 // ------------------------------------------------------------------ joining partial results
 // out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the runs that share
-// a unit; blockIdx.x is the run in which the unit ends.  A warp takes 32 rows
-// of N 16-byte pieces (neighbours in a chunk of one writing warp).  The runs
-// are read CH at a time, maxima, sums and pieces at once (one memory round trip
-// per chunk); the running maximum rescales what earlier chunks added.
+// a unit.  A warp takes 32 rows of N 16-byte pieces (neighbours in a chunk of
+// one writing warp) at a time.  The runs are read CH at a time, maxima, sums
+// and pieces at once (one memory round trip per chunk); the running maximum
+// rescales what earlier chunks added.  Two CTAs an SM that walk over the pieces:
+// 1184 small ones took 6 us to start, more than their work.
+constexpr int JOIN_THREADS = 512, JOIN_CTAS = 2 * 148;
 template <int N, int CH>
-__global__ void __launch_bounds__(256)
-tree_join_kernel(const __grid_constant__ Args a) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(JOIN_THREADS, 2)
+tree_join_kernel(const __grid_constant__ Args a, int runs) {
+    const int lane = threadIdx.x & 31;
+    constexpr int PIECES = 512 / N;              // of a unit
     pdl_trigger();
     pdl_wait();
-    const int4 join = __ldg(a.joins + blockIdx.x);
-    const int p0 = join.w, p1 = blockIdx.x;
-    const int piece = blockIdx.y * 8 + warp;
-    const int at = piece % (8 / N) * N, c = piece / (8 / N) & 1, owner = piece / (16 / N) & 15, rank = piece / (256 / N);
-    const int m = rank * HROWS + (owner & 1) * 32 + lane;
-    if (m >= join.z) return;
-    float top = -INFINITY, l = 0.f;
-    float4 o[N];
+    for (int item = blockIdx.x * (JOIN_THREADS / 32) + (threadIdx.x >> 5); item < runs * PIECES;
+         item += JOIN_CTAS * (JOIN_THREADS / 32)) {
+        const int p1 = item / PIECES, piece = item % PIECES;
+        const int4 join = __ldg(a.joins + p1);       // the unit that ends in run p1
+        const int p0 = join.w;
+        const int at = piece % (8 / N) * N, c = piece / (8 / N) & 1, owner = piece / (16 / N) & 15, rank = piece / (256 / N);
+        const int m = rank * HROWS + (owner & 1) * 32 + lane;
+        if (m >= join.z) continue;
+        float top = -INFINITY, l = 0.f;
+        float4 o[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p = p0; p <= p1; p += CH) {
-        float2 ml[CH];
-        uint4 v[CH][N];
+        for (int i = 0; i < N; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = p0; p <= p1; p += CH) {
+            float2 ml[CH];
+            uint4 v[CH][N];
 #pragma unroll
-        for (int c2 = 0; c2 < CH; ++c2) {
-            // slot of a run: 1 where the unit begins in it, 0 where it continues the unit
-            const bool there = p + c2 <= p1;
-            const int slot = 2 * (p + c2) + (p + c2 == p0);
-            ml[c2] = there ? __ldg(a.part_ml + slot * MROWS + m) : make_float2(-INFINITY, 0.f);
+            for (int c2 = 0; c2 < CH; ++c2) {
+                // slot of a run: 1 where the unit begins in it, 0 where it continues the unit
+                const bool there = p + c2 <= p1;
+                const int slot = 2 * (p + c2) + (p + c2 == p0);
+                ml[c2] = there ? __ldg(a.part_ml + slot * MROWS + m) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                v[c2][i] = there ? __ldg(a.part_o + part_at(slot, rank, owner, c, at + i, lane)) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        float mc = top;
+                for (int i = 0; i < N; ++i)
+                    v[c2][i] = there ? __ldg(a.part_o + part_at(slot, rank, owner, c, at + i, lane)) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            float mc = top;
 #pragma unroll
-        for (int c2 = 0; c2 < CH; ++c2) mc = fmaxf(mc, ml[c2].x);
-        const float scale = top == mc ? 1.f : ex2_approx(top - mc);
-        l *= scale;
+            for (int c2 = 0; c2 < CH; ++c2) mc = fmaxf(mc, ml[c2].x);
+            const float scale = top == mc ? 1.f : ex2_approx(top - mc);
+            l *= scale;
 #pragma unroll
-        for (int i = 0; i < N; ++i) { o[i].x *= scale; o[i].y *= scale; o[i].z *= scale; o[i].w *= scale; }
-        top = mc;
+            for (int i = 0; i < N; ++i) { o[i].x *= scale; o[i].y *= scale; o[i].z *= scale; o[i].w *= scale; }
+            top = mc;
 #pragma unroll
-        for (int c2 = 0; c2 < CH; ++c2) {
-            // a run that saw nothing of the row has weight 0 (its sum is 0, or a NaN that stays)
-            const float wgt = ml[c2].x == -INFINITY ? (ml[c2].y == 0.f ? 0.f : 1.f) : ex2_approx(ml[c2].x - top);
-            l += wgt * ml[c2].y;
+            for (int c2 = 0; c2 < CH; ++c2) {
+                // a run that saw nothing of the row has weight 0 (its sum is 0, or a NaN that stays)
+                const float wgt = ml[c2].x == -INFINITY ? (ml[c2].y == 0.f ? 0.f : 1.f) : ex2_approx(ml[c2].x - top);
+                l += wgt * ml[c2].y;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                o[i].x += wgt * __uint_as_float(v[c2][i].x); o[i].y += wgt * __uint_as_float(v[c2][i].y);
-                o[i].z += wgt * __uint_as_float(v[c2][i].z); o[i].w += wgt * __uint_as_float(v[c2][i].w);
+                for (int i = 0; i < N; ++i) {
+                    o[i].x += wgt * __uint_as_float(v[c2][i].x); o[i].y += wgt * __uint_as_float(v[c2][i].y);
+                    o[i].z += wgt * __uint_as_float(v[c2][i].z); o[i].w += wgt * __uint_as_float(v[c2][i].w);
+                }
             }
         }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t first = (int64_t)(((uint64_t)(uint32_t)join.y << 32) | (uint32_t)join.x);
-    uint2* d = reinterpret_cast<uint2*>(a.out + (first + m) * DV + part_col(owner, c) + 4 * at);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t first = (int64_t)(((uint64_t)(uint32_t)join.y << 32) | (uint32_t)join.x);
+        uint2* d = reinterpret_cast<uint2*>(a.out + (first + m) * DV + part_col(owner, c) + 4 * at);
 #pragma unroll
-    for (int i = 0; i < N; ++i) d[i] = make_uint2(bf16_pair(o[i].x * inv, o[i].y * inv), bf16_pair(o[i].z * inv, o[i].w * inv));
+        for (int i = 0; i < N; ++i) d[i] = make_uint2(bf16_pair(o[i].x * inv, o[i].y * inv), bf16_pair(o[i].z * inv, o[i].w * inv));
+    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -1105,7 +1120,7 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int box_rows) {
 
 // What the host knows of the list of blocks: at most this many.
 struct Plan {
-    int units, list_blocks, pairs;
+    int units, list_blocks, pairs, sharing;
     int64_t blocks;
 };
 Plan plan(const ic_paged_rows& pr, int k, int Hq) {
@@ -1114,6 +1129,15 @@ Plan plan(const ic_paged_rows& pr, int k, int Hq) {
     p.list_blocks = k ? ceil_div(k, NB) : (int)ceil_div64(pr.T_max, NB);
     p.blocks = (int64_t)pr.B * p.units * p.list_blocks;
     p.pairs = (int)std::min<int64_t>(MAX_PAIRS, p.blocks);
+    p.sharing = BY_LENGTH;
+    if (k && p.blocks > 0) {
+        const int64_t units = p.blocks / p.list_blocks, nt = p.list_blocks, P = p.pairs;
+        const int64_t parts = std::max<int64_t>(1, P / units), run = ceil_div64(p.blocks, P);
+        const int64_t whole = ceil_div64(units, P) * (nt + UNIT_COST);
+        const int64_t in_parts = units > P ? INT64_MAX : ceil_div64(nt, parts) + UNIT_COST + JOIN_COST;
+        const int64_t in_runs = run + (ceil_div64(run - 1, nt) + 1) * UNIT_COST + JOIN_COST;
+        p.sharing = whole <= std::min(in_parts, in_runs) ? WHOLE : in_parts <= in_runs ? PARTS : RUNS;
+    }
     return p;
 }
 
@@ -1154,6 +1178,7 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
     a.num_pages = pr.num_pages;
     a.units = p.units;
     a.list_blocks = p.list_blocks;
+    a.sharing = p.sharing;
     a.scale_log2 = scale * LOG2E;
     if (cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES) != cudaSuccess)
         return cuda_error("tree_attn_q8");
@@ -1162,12 +1187,12 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
         return cuda_error("tree_attn_q8");
     count_launch(IC_LK_TREE);
     ic_status st = last_launch_status();
-    if (st != IC_OK || p.list_blocks == 1) return st;        // units of one block are always whole
+    if (st != IC_OK || p.sharing == WHOLE || p.list_blocks == 1) return st;     // no partial results
     // few runs: one piece a warp, for the latency of many runs of one unit; else
     // four, for fewer warps
     const bool few = p.pairs <= 32;
     auto join = few ? tree_join_kernel<1, 8> : tree_join_kernel<4, 2>;
-    if (launch_ex(join, dim3((unsigned)p.pairs, few ? 64 : 16), dim3(256), 0, s, pdl, 0, a) != cudaSuccess)
+    if (launch_ex(join, dim3(JOIN_CTAS), dim3(JOIN_THREADS), 0, s, pdl, 0, a, p.pairs) != cudaSuccess)
         return cuda_error("tree_join");
     count_launch(IC_LK_COMBINE);
     return last_launch_status();

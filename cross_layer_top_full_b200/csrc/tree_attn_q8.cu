@@ -157,7 +157,7 @@ __device__ __forceinline__ int total_blocks(const Args& a) {
 //   WHOLE  the units, whole, in equal shares (nothing to join)
 //   PARTS  each unit over parts_of() pairs, in proportion to its blocks; a pair
 //          has one unit
-//   RUNS   the list of blocks in equal runs, over the units' borders
+//   RUNS   the list of all units' costs in equal runs, over the units' borders
 // Lists are all of one length: the host takes the cheapest.  With every
 // position the lengths are known on the device, which decides between PARTS
 // and RUNS.  Measured: 32 lists of 2048 (16 blocks), PARTS 25 us, RUNS 33;
@@ -166,12 +166,44 @@ enum { WHOLE, PARTS, RUNS, BY_LENGTH };
 constexpr int UNIT_COST = 3, JOIN_COST = 4;
 __device__ __forceinline__ int parts_of(const Args& a, int b, int n, int P) { return max(1, blocks_of(a, b) * P / n); }
 
-// Equal runs: n blocks over P pairs, the first n % P one block longer.
+// Equal shares: n things over P pairs, the first n % P one more.
 __device__ __forceinline__ int pairs_of(int n, int max_pairs) { return min(n, max_pairs); }
 __device__ __forceinline__ int run_begin(int n, int P, int p) { return n / P * p + min(n % P, p); }
 __device__ __forceinline__ int pair_with(int n, int P, int t) {
     const int q = n / P, longer = n % P, at = longer * (q + 1);
     return t < at ? t / (q + 1) : longer + (t - at) / q;
+}
+
+// Where place v of the list of shares lies (PARTS: a unit counts as its parts,
+// RUNS: as its blocks and UNIT_COST before them): sequence b (a.B: past the
+// end), place o from its first, blocks before the sequence.  One warp.
+struct Place {
+    int b, o, blocks;
+};
+__device__ __forceinline__ Place locate(const Args& a, int v, bool parts, int n, int P) {
+    if (a.idx) {
+        const int per = a.units * (parts ? parts_of(a, 0, n, P) : a.list_blocks + UNIT_COST);
+        const int b = min(v / per, a.B);
+        return {b, v - b * per, b * a.units * a.list_blocks};
+    }
+    Place r{a.B, v, 0};
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.B && r.b == a.B; b0 += 32) {
+        const int at = b0 + (threadIdx.x & 31), nt = at < a.B ? blocks_of(a, at) : 0;
+        const int c = at >= a.B ? 0 : (parts ? parts_of(a, at, n, P) : nt + UNIT_COST) * a.units;
+        int x = c, y = nt * a.units;         // inclusive prefix sums
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x2 = __shfl_up_sync(0xffffffffu, x, o), y2 = __shfl_up_sync(0xffffffffu, y, o);
+            if ((threadIdx.x & 31) >= o) { x += x2; y += y2; }
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, r.o < x);
+        const int l = hit ? __ffs(hit) - 1 : 31;
+        r.o -= __shfl_sync(0xffffffffu, hit ? x - c : x, l);
+        r.blocks += __shfl_sync(0xffffffffu, hit ? y - nt * a.units : y, l);
+        if (hit) r.b = b0 + l;
+    }
+    return r;
 }
 
 // A walk over a run: unit u of sequence b, from block t on.
@@ -498,63 +530,49 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             }
             used = __reduce_add_sync(0xffffffffu, used) * a.units;
             longest = __reduce_max_sync(0xffffffffu, longest);
-            parts = used <= P && longest <= (n + P - 1) / P + UNIT_COST;
+            parts = used <= P && longest <= (n + UNIT_COST * a.B * a.units) / P;
         }
-        // this pair's place in the list of parts, or its first block in the list of blocks
-        int off = parts ? p : 0, left = 0, begin = 0;
+        int b = a.B, u = 0, t = 0, left = 0, from = 0;
+        bool ends = false;           // the unit that the run begins inside ends in it; `from`: its first pair
         if (a.sharing == WHOLE) {
-            const int units = a.B * a.units;
-            if (p < min(units, P)) {
-                off = begin = run_begin(units, min(units, P), p) * a.list_blocks;
-                left = run_begin(units, min(units, P), p + 1) * a.list_blocks - begin;
+            const int units = a.B * a.units, P1 = min(units, P), first = run_begin(units, P1, min(p, P1));
+            b = first / a.units;
+            u = first % a.units;
+            left = p < P1 ? (run_begin(units, P1, p + 1) - first) * a.list_blocks : 0;
+        } else if (parts) {
+            const Place at = locate(a, p, true, n, P);
+            b = at.b;
+            if (b < a.B) {
+                const int nt = blocks_of(a, b), k = parts_of(a, b, n, P), i = at.o % k;
+                u = at.o / k;
+                t = run_begin(nt, k, i);
+                left = run_begin(nt, k, i + 1) - t;
+                ends = k > 1 && i == k - 1;
+                from = p - i;
             }
-        } else if (!parts && p < P) {
-            off = begin = run_begin(n, P, p);
-            left = run_begin(n, P, p + 1) - begin;
-        }
-        int b = a.B;                 // the sequence that off lies in (a.B: none), off then counts from its first
-        if (a.idx) {
-            const int per = a.units * (parts ? parts_of(a, 0, n, P) : a.list_blocks);
-            b = parts || left > 0 ? min(off / per, a.B) : a.B;
-            off %= per;
-        } else if (parts || left > 0) {
-            for (int b0 = 0; b0 < a.B && b == a.B; b0 += 32) {
-                const int at = b0 + lane;
-                const int c = at >= a.B ? 0 : (parts ? parts_of(a, at, n, P) : blocks_of(a, at)) * a.units;
-                const int sum = __reduce_add_sync(0xffffffffu, c);
-                if (off >= sum) {
-                    off -= sum;
-                    continue;
+        } else if (p < P) {
+            const int all = n + UNIT_COST * a.B * a.units;
+            int end = n, inside = 0;         // the run's last block + 1; how far into its unit it begins
+#pragma unroll 1
+            for (int e = 1; e >= 0; --e) {
+                const int v = run_begin(all, P, p + e);
+                const Place at = locate(a, v, false, n, P);
+                if (at.b == a.B) continue;
+                const int nt = blocks_of(a, at.b);
+                b = at.b;
+                u = at.o / (nt + UNIT_COST);
+                inside = at.o % (nt + UNIT_COST);
+                t = max(0, inside - UNIT_COST);
+                const int block = at.blocks + u * nt + t;
+                if (e) end = block;
+                else {
+                    left = end - block;
+                    ends = t > 0 && left >= nt - t;
+                    if (ends) from = pair_with(all, P, v - inside + UNIT_COST);
                 }
-                int x = c;           // inclusive prefix sum
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += y;
-                }
-                const int l = __ffs(__ballot_sync(0xffffffffu, off < x)) - 1;
-                b = b0 + l;
-                off -= __shfl_sync(0xffffffffu, x - c, l);
             }
         }
         if (lane == 0) {
-            int u = 0, t = 0, from = 0;
-            bool ends = false;       // the unit that the run begins inside ends in it; `from`: its first pair
-            if (b < a.B) {
-                const int nt = blocks_of(a, b);
-                if (parts) {
-                    const int k = parts_of(a, b, n, P), i = off % k;
-                    u = off / k;
-                    t = run_begin(nt, k, i);
-                    left = run_begin(nt, k, i + 1) - t;
-                    ends = k > 1 && i == k - 1;
-                    from = p - i;
-                } else {
-                    u = off / nt;
-                    t = off % nt;
-                    ends = t > 0 && left >= nt - t;
-                    if (ends) from = pair_with(n, P, begin - t);
-                }
-            }
             s.start_b = min(b, a.B - 1);
             s.start_u = u;
             s.start_t = t;
@@ -1132,10 +1150,10 @@ Plan plan(const ic_paged_rows& pr, int k, int Hq) {
     p.sharing = BY_LENGTH;
     if (k && p.blocks > 0) {
         const int64_t units = p.blocks / p.list_blocks, nt = p.list_blocks, P = p.pairs;
-        const int64_t parts = std::max<int64_t>(1, P / units), run = ceil_div64(p.blocks, P);
+        const int64_t parts = std::max<int64_t>(1, P / units), run = ceil_div64(units * (nt + UNIT_COST), P);
         const int64_t whole = ceil_div64(units, P) * (nt + UNIT_COST);
         const int64_t in_parts = units > P ? INT64_MAX : ceil_div64(nt, parts) + UNIT_COST + JOIN_COST;
-        const int64_t in_runs = run + (ceil_div64(run - 1, nt) + 1) * UNIT_COST + JOIN_COST;
+        const int64_t in_runs = run + UNIT_COST + JOIN_COST;
         p.sharing = whole <= std::min(in_parts, in_runs) ? WHOLE : in_parts <= in_runs ? PARTS : RUNS;
     }
     return p;
@@ -1152,7 +1170,7 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
                               void* out, uint32_t* status, void* scratch, cudaStream_t s) {
     const Plan p = plan(pr, k, Hq);
     const int64_t all_units = (int64_t)pr.B * p.units;
-    if ((int64_t)pr.B * pr.Lq > 0x7fffffffLL || p.blocks > 0x7fffffffLL) return IC_ERR_UNSUPPORTED;
+    if ((int64_t)pr.B * pr.Lq > 0x7fffffffLL || p.blocks >= 1 << 29) return IC_ERR_UNSUPPORTED;
     CUtensorMap map_box;
     if (!make_map(&map_box, kv_q8, (int64_t)pr.num_pages * pr.page_size, 64)) return cuda_error("tree_attn_q8");
     Args a;

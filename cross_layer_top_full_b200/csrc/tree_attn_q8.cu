@@ -1048,8 +1048,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
 // a unit.  A warp takes 32 rows of N 16-byte pieces (neighbours in a chunk of
 // one writing warp) at a time.  The runs are read CH at a time, maxima, sums
 // and pieces at once (one memory round trip per chunk); the running maximum
-// rescales what earlier chunks added.  Two CTAs an SM that walk over the pieces:
-// 1184 small ones took 6 us to start, more than their work.
+// rescales what earlier chunks added.  Bound by latency (31 MB of 8 runs a unit
+// took 10 us as 1184 small CTAs, of which 6 to start them, and as long with a
+// list entry read before each piece): two CTAs an SM walk over the pieces, and
+// the list of what there is to join is read once.
 constexpr int JOIN_THREADS = 512, JOIN_CTAS = 2 * 148;
 template <int N, int CH>
 __global__ void __launch_bounds__(JOIN_THREADS, 2)
@@ -1058,11 +1060,29 @@ tree_join_kernel(const __grid_constant__ Args a, int runs) {
     constexpr int PIECES = 512 / N;              // of a unit
     pdl_trigger();
     pdl_wait();
-    for (int item = blockIdx.x * (JOIN_THREADS / 32) + (threadIdx.x >> 5); item < runs * PIECES;
+    __shared__ int4 joins[MAX_PAIRS];
+    __shared__ int ends[MAX_PAIRS], count;
+    if (threadIdx.x < 32) {
+        int n = 0;
+        for (int p = lane; p - lane < runs; p += 32) {
+            const int4 join = p < runs ? __ldg(a.joins + p) : make_int4(0, 0, 0, 0);
+            const unsigned there = __ballot_sync(0xffffffffu, join.z > 0);
+            if (join.z > 0) {
+                const int at = n + __popc(there & ((1u << lane) - 1u));
+                joins[at] = join;
+                ends[at] = p;
+            }
+            n += __popc(there);
+        }
+        if (lane == 0) count = n;
+    }
+    __syncthreads();
+    const int items = count * PIECES;
+    for (int item = blockIdx.x * (JOIN_THREADS / 32) + (threadIdx.x >> 5); item < items;
          item += JOIN_CTAS * (JOIN_THREADS / 32)) {
-        const int p1 = item / PIECES, piece = item % PIECES;
-        const int4 join = __ldg(a.joins + p1);       // the unit that ends in run p1
-        const int p0 = join.w;
+        const int piece = item % PIECES;
+        const int4 join = joins[item / PIECES];
+        const int p0 = join.w, p1 = ends[item / PIECES];       // the unit's runs
         const int at = piece % (8 / N) * N, c = piece / (8 / N) & 1, owner = piece / (16 / N) & 15, rank = piece / (256 / N);
         const int m = rank * HROWS + (owner & 1) * 32 + lane;
         if (m >= join.z) continue;
@@ -1207,9 +1227,9 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
     ic_status st = last_launch_status();
     if (st != IC_OK || p.sharing == WHOLE || p.list_blocks == 1) return st;     // no partial results
     // few runs: one piece a warp, for the latency of many runs of one unit; else
-    // four, for fewer warps
+    // two, for fewer warps
     const bool few = p.pairs <= 32;
-    auto join = few ? tree_join_kernel<1, 8> : tree_join_kernel<4, 2>;
+    auto join = few ? tree_join_kernel<1, 8> : tree_join_kernel<2, 4>;
     if (launch_ex(join, dim3(JOIN_CTAS), dim3(JOIN_THREADS), 0, s, pdl, 0, a, p.pairs) != cudaSuccess)
         return cuda_error("tree_join");
     count_launch(IC_LK_COMBINE);

@@ -482,6 +482,14 @@ __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t
     return sq[row];
 }
 
+// Sends for the next unit's rows while this unit's blocks are under way.
+__device__ __forceinline__ void prefetch_q(const Args& a, const Rows& r, uint32_t rank) {
+    const int lines = min(HROWS, r.rows - (int)rank * HROWS) * (KVW * 2 / 128);      // 9 lines of 128 bytes a row
+    const uint8_t* q = reinterpret_cast<const uint8_t*>(a.q + (r.first + rank * HROWS) * KVW);
+    for (int i = threadIdx.x; i < lines; i += 32 * SOFT_WARPS)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(q + (int64_t)i * 128));
+}
+
 // ------------------------------------------------------------------ the kernel
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 rows x 128 bytes
@@ -682,6 +690,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             }
             const float arow = sq * a.scale_log2;
             const uint64_t a2 = f2(arow, arow);
+            if (w.left > n) {
+                Walk after = w;
+                after.next(a);
+                prefetch_q(a, unit_rows(a, after.b, after.u), rank);
+            }
             mref = -INFINITY;       // what this group's l is relative to
             l = 0.f;
             for (int x = 0; x < n; ++x, ++j) {

@@ -27,29 +27,31 @@ template <typename T> struct Vec;   // the values of one 16-byte vector
 template <> struct Vec<float> { static constexpr int N = 4; };
 template <> struct Vec<__nv_bfloat16> { static constexpr int N = 8; };
 
-// N values at p: one 16-byte load where rows start on 16-byte boundaries
-// (ALIGNED), else element loads.
+// N values at p, as they lie: one 16-byte load where rows start on 16-byte
+// boundaries (ALIGNED), else element loads.
 template <bool ALIGNED>
-__device__ __forceinline__ void load_vec(const float* p, float (&x)[4]) {
-    if (ALIGNED) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = __ldg(p + i);
-    }
+__device__ __forceinline__ uint4 load_vec(const float* p) {
+    if (ALIGNED) return __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(p);
+    return make_uint4(__ldg(u), __ldg(u + 1), __ldg(u + 2), __ldg(u + 3));
 }
 template <bool ALIGNED>
-__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&x)[8]) {
+__device__ __forceinline__ uint4 load_vec(const __nv_bfloat16* p) {
+    if (ALIGNED) return __ldg(reinterpret_cast<const uint4*>(p));
+    const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
     uint32_t w[4];
-    if (ALIGNED) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else {
-        const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = (uint32_t)__ldg(u + 2 * i) | (uint32_t)__ldg(u + 2 * i + 1) << 16;
-    }
+    for (int i = 0; i < 4; ++i) w[i] = (uint32_t)__ldg(u + 2 * i) | (uint32_t)__ldg(u + 2 * i + 1) << 16;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The values of a vector.
+__device__ __forceinline__ void values_of(const uint4& v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void values_of(const uint4& v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         x[2 * i] = __uint_as_float(w[i] << 16);
@@ -110,9 +112,11 @@ __device__ __forceinline__ void decode_codes(const uint32_t (&w)[N / 4], float s
     }
 }
 
-// Largest finite magnitude of a lane's values, as bits.
+// Largest finite magnitude of a vector's values, as bits.
 template <int N>
-__device__ __forceinline__ uint32_t lane_max(const float (&x)[N]) {
+__device__ __forceinline__ uint32_t vec_max(const uint4& v) {
+    float x[N];
+    values_of(v, x);
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) m = max(m, finite_abs_bits(x[i]));
@@ -142,42 +146,48 @@ cache_write_kernel(const T* __restrict__ kv, int64_t kv_stride, const T* __restr
     pdl_trigger();
     pdl_wait();
     if (n >= n_rows) return;
-    float x[IT][N], rope[N], key[N];
+    // kept as they lie until they are used: 32 registers, a full SM of warps
+    uint4 x[IT], rope, key = make_uint4(0u, 0u, 0u, 0u);
     if (kv) {
         const T* p = kv + n * kv_stride;
 #pragma unroll
-        for (int i = 0; i < IT; ++i) load_vec<ALIGNED>(p + (i * 32 + lane) * N, x[i]);
-        if (lane < DR / N) load_vec<ALIGNED>(p + DV + lane * N, rope);
+        for (int i = 0; i < IT; ++i) x[i] = load_vec<ALIGNED>(p + (i * 32 + lane) * N);
+        if (lane < DR / N) rope = load_vec<ALIGNED>(p + DV + lane * N);
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) key[i] = 0.f;
-    if (k_idx && lane < DI / N) load_vec<ALIGNED>(k_idx + n * k_stride + lane * N, key);
+    if (k_idx && lane < DI / N) key = load_vec<ALIGNED>(k_idx + n * k_stride + lane * N);
     const int64_t slot = slot_of(slots, n, num_rows, status);
     if (slot < 0) return;
+    float y[N];
     if (kv) {
         uint8_t* row = kv_q8 + slot * ROW;
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < IT; ++i) m = max(m, lane_max<N>(x[i]));
+        for (int i = 0; i < IT; ++i) m = max(m, vec_max<N>(x[i]));
         const int e = scale_exponent(__reduce_max_sync(0xffffffffu, m));
+        const float inv = exp2_int(-e);
 #pragma unroll
-        for (int i = 0; i < IT; ++i) store_codes<N>(row + (i * 32 + lane) * N, x[i], exp2_int(-e));
+        for (int i = 0; i < IT; ++i) {
+            values_of(x[i], y);
+            store_codes<N>(row + (i * 32 + lane) * N, y, inv);
+        }
         if (lane == 0) kv_scale[slot] = exp2_int(e);
         if (lane < DR / N) {
             uint32_t* d = reinterpret_cast<uint32_t*>(row + OFF_ROPE) + lane * (N / 2);
+            values_of(rope, y);
 #pragma unroll
-            for (int i = 0; i < N; ++i) rope[i] *= exp2_int(-e);
+            for (int i = 0; i < N; ++i) y[i] *= inv;
             if constexpr (N == 8) {
-                *reinterpret_cast<uint4*>(d) = make_uint4(bf16_pair(rope[0], rope[1]), bf16_pair(rope[2], rope[3]),
-                                                          bf16_pair(rope[4], rope[5]), bf16_pair(rope[6], rope[7]));
+                *reinterpret_cast<uint4*>(d) = make_uint4(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]),
+                                                          bf16_pair(y[4], y[5]), bf16_pair(y[6], y[7]));
             } else {
-                *reinterpret_cast<uint2*>(d) = make_uint2(bf16_pair(rope[0], rope[1]), bf16_pair(rope[2], rope[3]));
+                *reinterpret_cast<uint2*>(d) = make_uint2(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]));
             }
         }
     }
     if (k_idx) {
-        const int e = scale_exponent(__reduce_max_sync(0xffffffffu, lane_max<N>(key)));
-        if (lane < DI / N) store_codes<N>(k_codes + slot * DI + lane * N, key, exp2_int(-e));
+        const int e = scale_exponent(__reduce_max_sync(0xffffffffu, vec_max<N>(key)));
+        values_of(key, y);
+        if (lane < DI / N) store_codes<N>(k_codes + slot * DI + lane * N, y, exp2_int(-e));
         if (lane == 0) k_scale[slot] = exp2_int(e);
     }
 }

@@ -85,7 +85,7 @@ constexpr int OFF_XL = OFF_XM;                        // [8][64] float: row sums
 constexpr int OFF_MR = OFF_XM + 2 * 4 * HROWS * 4;    // [2][64] float: running maxima after a block
 constexpr int OFF_SQ = OFF_MR + 2 * HROWS * 4;        // [64] float: scales of Q's rows
 constexpr int OFF_BARS = OFF_SQ + HROWS * 4;
-constexpr int GROUP_WARPS = 8, SOFT_WARPS = 16, W_COPY = 16, W_RES = 20, W_S = 22, W_PV = 23;
+constexpr int GROUP_WARPS = 8, SOFT_WARPS = 16, W_COPY = 16, W_RES = 20, W_S = 22;
 constexpr int THREADS = 32 * 24;
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 384, TM_QR = TM_Q + 96;   // TM_Q: lo 1-3, the bfloat16 columns
 constexpr int TMEM_COLS = 512;
@@ -241,45 +241,6 @@ __device__ __forceinline__ Rows unit_rows(const Args& a, int b, int u) {
     }
     r.first = (int64_t)b * a.Lq * a.Hq + r.node0;
     return r;
-}
-
-// ------------------------------------------------------------------ waits
-// Bounded like those of sm100.cuh (about a second in all), but four
-// instructions a poll: two dozen warps wait here most of the time, and longer
-// polls kept the instruction fetch from the warps that work.  Every lane waits,
-// and every lane gets the same answer.
-__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 4096;\n"
-        "WAIT:\n\t"
-        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-        "@p bra DONE;\n\t"
-        "sub.u32 n, n, 1;\n\t"
-        "setp.ne.u32 q, n, 0;\n\t"
-        "@q bra WAIT;\n"
-        "DONE:\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* abort, uint32_t site) {
-    const uint64_t t0 = globaltimer();
-    while (true) {
-        if (__all_sync(0xffffffffu, poll(bar, parity))) return true;
-        if (__any_sync(0xffffffffu, *abort != 0)) return false;
-        if (__any_sync(0xffffffffu, globaltimer() - t0 > IC_WAIT_LIMIT_NS)) {
-            if ((threadIdx.x & 31) == 0) flag_timeout(status, site);
-            *abort = 1;
-            return false;
-        }
-    }
-}
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort, uint32_t site) {
-    if (__all_sync(0xffffffffu, poll(smem_u32(bar), parity))) return true;
-    return wait_on(smem_u32(bar), parity, status, abort, site);
 }
 
 // ------------------------------------------------------------------ small helpers

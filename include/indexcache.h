@@ -107,9 +107,9 @@ ic_status ic_read_status(void* ws, void* stream, int32_t* device_status);
  * (the error of the lowest set bit). */
 ic_status ic_check_status(void* ws, void* stream);
 
-/* Failure-path self-test: launches one CTA whose pipeline wait (the
- * library's bounded mbarrier wait) never completes.  After about 1 s the
- * wait gives up, bit 1 (wait timeout) of the status word of `ws` is set and
+/* Failure-path self-test: launches one CTA whose pipeline waits (the
+ * library's two bounded mbarrier waits) never complete.  After about 1 s they
+ * give up, bit 1 (wait timeout) of the status word of `ws` is set and
  * the kernel returns normally; read it with ic_read_status.  Faults and
  * hangs nothing; the context stays usable.  ws_bytes >= IC_STATUS_BYTES. */
 ic_status ic_selftest_wait_timeout(void* ws, size_t ws_bytes, void* stream);
@@ -508,6 +508,8 @@ ic_status ic_cache_read_q8(const void* kv_q8, const float* kv_scale, const void*
  *             nothing gets zeros.
  * A NaN or infinity in a cache row that a query row does not see does not
  * reach that row's output; a NaN in a seen row makes it NaN.
+ * Batches of 2^29 blocks or more (blocks of 128 positions of T_max or of k, for
+ * each row of a list or each 128 (node, head) pairs) return IC_ERR_UNSUPPORTED.
  * Workspace: ic_tree_attn_q8_workspace_size(pr, k, Hq). */
 size_t ic_tree_attn_q8_workspace_size(const ic_paged_rows* pr, int k, int Hq);
 ic_status ic_tree_attn_q8_paged(const void* q, const void* kv_q8, const float* kv_scale,

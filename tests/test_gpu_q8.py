@@ -382,6 +382,29 @@ def test_rows_of_very_different_sizes(k, dev):
     b.check(b.run())
 
 
+def test_many_small_weights_beside_a_large_one(dev):
+    """One position outweighs each of 6000 others by 2^16, and they hold a third of its weight together:
+    none of them may be lost."""
+    b = Tree([6001], 1, dev, seed=47, Hq=128)
+    u = np.zeros(576)
+    u[540:560] = 1.0                           # the logits come from columns that carry no value
+    q = num(b.q) * 0
+    q[0, 0] = u
+    b.q = torch.from_numpy(q).to(BF)
+    for s in range(6001):
+        x = np.zeros(576)
+        x[:512] = 1.0 + 0.5 * np.sin(s + np.arange(512)) if s else -1.0
+        x[540:560] = 24.0 * np.log(2.0 ** 16 / 4) / 20 if s == 0 else 0.0
+        r, sc = u8.pack_rows(x[None])
+        b.rows[0][s], b.scales[0][s] = r[0], sc[0]
+    b.place()
+    b.scale = 1.0 / 24
+    out = b.run()
+    b.check(out)
+    share = 6000 / (6000 + 2.0 ** 14)
+    assert abs(float(out.float().mean()) - (2 * share - 1)) < 0.02
+
+
 def test_growing_logits_rescale(dev):
     """Later positions win by ever larger steps: the running maximum moves in every block."""
     b = Tree([1500], 2, dev, seed=23, Hq=128)
@@ -521,6 +544,70 @@ def test_a_full_gpu_of_rows(dev):
     one.B, one.q, one.idx, one.masks, one.table = 1, one.q[39:], one.idx[39:], one.masks[39:], one.table[39:]
     alone = one.run()
     np.testing.assert_allclose(num(alone[0]), num(out[39]), rtol=2.0 ** -6, atol=2.0 ** -8)
+
+
+def test_more_lists_than_the_gpu_has_pairs(dev):
+    """80 lists of 16 blocks: the CTA pairs take equal runs over the lists' borders; most blocks name nothing."""
+    b = Tree([40 + 3 * i for i in range(80)], 1, dev, seed=42, Hq=33, k=2048)
+    b.check(b.run(), rows={(i, 0) for i in (0, 1, 2, 17, 36, 37, 38, 55, 78, 79)})
+
+
+def test_a_list_over_many_pairs(dev):
+    b = Tree([20000], 1, dev, seed=43, Hq=5, k=16384)
+    b.check(b.run())
+
+
+@pytest.mark.parametrize("lens,Lq,Hq,T_max", [
+    ([64 + 61 * i for i in range(40)], 16, 16, None),       # 80 units over all pairs, several in one
+    ([9000, 20, 17, 4000], 8, 16, 100000),                  # shares by length; a bound far above the lengths
+    ([17] * 33 + [6000] * 3, 1, 128, 6001),                 # more sequences than lanes of a warp
+    ([3] * 100, 3, 128, None),                              # units of one block
+])
+def test_sharing_out_by_length(lens, Lq, Hq, T_max, dev):
+    b = Tree(lens, Lq, dev, seed=44, Hq=Hq, T_max=T_max)
+    rows = {(i, j) for i in (0, 1, len(lens) // 2, len(lens) - 2, len(lens) - 1) for j in (0, Lq - 1)}
+    b.check(b.run(), rows=rows)
+
+
+@pytest.mark.parametrize("k", [0, 256])
+def test_a_captured_call_follows_its_inputs(k, dev):
+    """The same graph replayed after the lengths, pages, trees and queries have changed in place."""
+    first = Tree([900, 40, 300], 4, dev, seed=45, Hq=48, k=k, T_max=2500)
+    then = Tree([30, 2500, 4], 4, dev, seed=46, Hq=48, k=k, T_max=2500)
+    want = [first.run().clone(), then.run().clone()]
+    rows = max(len(first.d_cache), len(then.d_cache))
+    cache = torch.zeros(rows, 640, dtype=torch.uint8, device=dev)
+    scale = torch.ones(rows, device=dev)
+    lens, table = first.d_lens.clone(), first.d_table.clone()
+    q, tree, idx = first.d_q.clone(), first.d_tree.clone(), None if not k else first.d_idx.clone()
+    pr = ic.paged_rows(lens, table, 2500, 128, rows // 128, 4)
+    ws = make_ws(ic.tree_attn_q8_workspace_size(pr, k, 48), dev)
+    out = torch.zeros_like(want[0])
+
+    def call():
+        ic.tree_attn_q8_paged(q, cache, scale, idx, pr, first.scale, out, ws, tree=tree)
+
+    cache[:len(first.d_cache)], scale[:len(first.d_cache)] = first.d_cache, first.d_scale
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            call()
+    torch.cuda.synchronize()
+    for turn in (1, 0, 1):
+        b = (first, then)[turn]
+        cache[:len(b.d_cache)], scale[:len(b.d_cache)] = b.d_cache, b.d_scale
+        for mine, theirs in ((lens, b.d_lens), (table, b.d_table), (q, b.d_q), (tree, b.d_tree)) + (((idx, b.d_idx),) if k else ()):
+            mine.copy_(theirs)
+        out.fill_(9)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[turn])
+    assert ic.read_status(ws) == 0
 
 
 # ---------------------------------------------------------------- refusals

@@ -280,6 +280,11 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ uint32_t bf16_pair2(uint64_t v) {
+    const float2 f = f2_split(v);
+    return bf16_pair(f.x, f.y);
+}
+
 // Two e4m3 numbers and two e5m2 numbers for what they leave of (a, b).
 __device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
     hi = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -425,6 +430,7 @@ __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t
         *reinterpret_cast<uint4*>(smem + OFF_P + 3 * ATOM + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
             make_uint4(w[0], w[1], w[2], w[3]);
     }
+    fence_async_smem();
     soft_sync();
     // to tensor memory: warps 4t..4t+3 take tile t
     const int row = (warp & 1) * 32 + lane, tile = warp >> 2;
@@ -436,18 +442,17 @@ __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t
     }
     tmem_st32(tmem + lane_base + TM_Q + 32 * tile, w);
     tmem_st_wait();
-    fence_async_smem();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive_remote_relaxed(q_bar);
     return sq[row];
 }
 
-// Sends for the next unit's rows while this unit's blocks are under way.
-__device__ __forceinline__ void prefetch_q(const Args& a, const Rows& r, uint32_t rank) {
+// Sends for a unit's rows ahead of load_q: thread i of n.
+__device__ __forceinline__ void prefetch_q(const Args& a, const Rows& r, uint32_t rank, int i, int n) {
     const int lines = min(HROWS, r.rows - (int)rank * HROWS) * (KVW * 2 / 128);      // 9 lines of 128 bytes a row
     const uint8_t* q = reinterpret_cast<const uint8_t*>(a.q + (r.first + rank * HROWS) * KVW);
-    for (int i = threadIdx.x; i < lines; i += 32 * SOFT_WARPS)
+    for (; i < lines; i += n)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(q + (int64_t)i * 128));
 }
 
@@ -541,6 +546,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 }
             }
         }
+        if (left > 0) prefetch_q(a, unit_rows(a, b, u), rank, lane, 32);
         if (lane == 0) {
             s.start_b = min(b, a.B - 1);
             s.start_u = u;
@@ -603,6 +609,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             }
             if (j > 0) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
+                const uint64_t inv2 = f2(inv, inv);
                 const bool ok = wait_for(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, status, abort, 9);
                 tc_fence_after();
                 if (w.left > 0) soft_sync();            // the staging area below is that of convert_q
@@ -619,7 +626,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                             uint32_t u[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                u[k] = bf16_pair(__uint_as_float(t[8 * i + 2 * k]) * inv, __uint_as_float(t[8 * i + 2 * k + 1]) * inv);
+                                u[k] = bf16_pair2(fmul2(f2(__uint_as_float(t[8 * i + 2 * k]), __uint_as_float(t[8 * i + 2 * k + 1])), inv2));
                             *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
                         }
                         __syncwarp();
@@ -654,7 +661,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             if (w.left > n) {
                 Walk after = w;
                 after.next(a);
-                prefetch_q(a, unit_rows(a, after.b, after.u), rank);
+                prefetch_q(a, unit_rows(a, after.b, after.u), rank, threadIdx.x, 32 * SOFT_WARPS);
             }
             mref = -INFINITY;       // what this group's l is relative to
             l = 0.f;
@@ -1024,11 +1031,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
 // and pieces at once (one memory round trip per chunk); the running maximum
 // rescales what earlier chunks added.  Bound by latency (31 MB of 8 runs a unit
 // took 10 us as 1184 small CTAs, of which 6 to start them, and as long with a
-// list entry read before each piece): two CTAs an SM walk over the pieces, and
-// the list of what there is to join is read once.
-constexpr int JOIN_THREADS = 512, JOIN_CTAS = 2 * 148;
-template <int N, int CH>
-__global__ void __launch_bounds__(JOIN_THREADS, 2)
+// list entry read before each piece): one or two CTAs an SM walk over the pieces,
+// and the list of what there is to join is read once.
+constexpr int JOIN_THREADS = 512;
+template <int N, int CH, int CTAS>
+__global__ void __launch_bounds__(JOIN_THREADS, CTAS)
 tree_join_kernel(const __grid_constant__ Args a, int runs) {
     const int lane = threadIdx.x & 31;
     constexpr int PIECES = 512 / N;              // of a unit
@@ -1053,7 +1060,7 @@ tree_join_kernel(const __grid_constant__ Args a, int runs) {
     __syncthreads();
     const int items = count * PIECES;
     for (int item = blockIdx.x * (JOIN_THREADS / 32) + (threadIdx.x >> 5); item < items;
-         item += JOIN_CTAS * (JOIN_THREADS / 32)) {
+         item += gridDim.x * (JOIN_THREADS / 32)) {
         const int piece = item % PIECES;
         const int4 join = joins[item / PIECES];
         const int p0 = join.w, p1 = ends[item / PIECES];       // the unit's runs
@@ -1163,7 +1170,6 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
                               const int32_t* idx, int k, const uint64_t* tree, const ic_paged_rows& pr, int Hq, float scale,
                               void* out, uint32_t* status, void* scratch, cudaStream_t s) {
     const Plan p = plan(pr, k, Hq);
-    const int64_t all_units = (int64_t)pr.B * p.units;
     if ((int64_t)pr.B * pr.Lq > 0x7fffffffLL || p.blocks >= 1 << 29) return IC_ERR_UNSUPPORTED;
     CUtensorMap map_box;
     if (!make_map(&map_box, kv_q8, (int64_t)pr.num_pages * pr.page_size, 64)) return cuda_error("tree_attn_q8");
@@ -1200,11 +1206,13 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
     count_launch(IC_LK_TREE);
     ic_status st = last_launch_status();
     if (st != IC_OK || p.sharing == WHOLE || p.list_blocks == 1) return st;     // no partial results
-    // few runs: one piece a warp, for the latency of many runs of one unit; else
-    // two, for fewer warps
+    // few runs: one piece a warp and every run at once, for the latency of many
+    // runs of one unit; else more pieces a warp, the fewer runs a unit has
+    // (8 a unit: 9.4 us with four pieces, 5.7 with two; 2 a unit: 5.3 and 7.0)
     const bool few = p.pairs <= 32;
-    auto join = few ? tree_join_kernel<1, 8> : tree_join_kernel<2, 4>;
-    if (launch_ex(join, dim3(JOIN_CTAS), dim3(JOIN_THREADS), 0, s, pdl, 0, a, p.pairs) != cudaSuccess)
+    const int64_t units = (int64_t)pr.B * p.units;
+    auto join = few ? tree_join_kernel<1, 16, 1> : p.pairs / units > 2 ? tree_join_kernel<2, 4, 2> : tree_join_kernel<4, 2, 2>;
+    if (launch_ex(join, dim3(few ? 148 : 2 * 148), dim3(JOIN_THREADS), 0, s, pdl, 0, a, p.pairs) != cudaSuccess)
         return cuda_error("tree_join");
     count_launch(IC_LK_COMBINE);
     return last_launch_status();

@@ -84,15 +84,36 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[8])
     }
 }
 
-// The N codes of one lane: 4 or 8 bytes.
-template <int N>
-__device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[N], float inv) {
-    uint32_t w[N / 4];
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i)
-        w[i] = encode2(x[4 * i], x[4 * i + 1], inv) | encode2(x[4 * i + 2], x[4 * i + 3], inv) << 16;
-    if constexpr (N == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(p) = w[0];
+// The codes of a vector's values times inv, a power of two: 4 or 8 bytes.
+// bfloat16 products with it are exact (what would fall under 2^-126 has the
+// code 0 either way), two at a time.
+__device__ __forceinline__ uint32_t mul_pair(uint32_t p, uint32_t inv2) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(p), "r"(inv2));
+    return r;
+}
+__device__ __forceinline__ uint32_t twice(float pow2) { return (__float_as_uint(pow2) >> 16) * 0x10001u; }
+__device__ __forceinline__ uint32_t encode_pair(uint32_t p) {
+    return encode2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u), 1.f);
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, const uint4& v, float inv, __nv_bfloat16) {
+    const uint32_t i2 = twice(inv);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(encode_pair(mul_pair(v.x, i2)) | encode_pair(mul_pair(v.y, i2)) << 16,
+                   encode_pair(mul_pair(v.z, i2)) | encode_pair(mul_pair(v.w, i2)) << 16);
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, const uint4& v, float inv, float) {
+    *reinterpret_cast<uint32_t*>(p) = encode2(__uint_as_float(v.x), __uint_as_float(v.y), inv) |
+                                      encode2(__uint_as_float(v.z), __uint_as_float(v.w), inv) << 16;
+}
+// The same values as bfloat16, rounded once: 16 or 8 bytes.
+__device__ __forceinline__ void store_scaled(uint8_t* p, const uint4& v, float inv, __nv_bfloat16) {
+    const uint32_t i2 = twice(inv);
+    *reinterpret_cast<uint4*>(p) = make_uint4(mul_pair(v.x, i2), mul_pair(v.y, i2), mul_pair(v.z, i2), mul_pair(v.w, i2));
+}
+__device__ __forceinline__ void store_scaled(uint8_t* p, const uint4& v, float inv, float) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(__uint_as_float(v.x) * inv, __uint_as_float(v.y) * inv),
+                                              bf16_pair(__uint_as_float(v.z) * inv, __uint_as_float(v.w) * inv));
 }
 template <int N>
 __device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t (&w)[N / 4]) {
@@ -112,15 +133,40 @@ __device__ __forceinline__ void decode_codes(const uint32_t (&w)[N / 4], float s
     }
 }
 
-// Largest finite magnitude of a vector's values, as bits.
+// Largest magnitude of a vector's values, as float32 bits: of all of them (two
+// instructions a pair; 0x7f800000 or more where one is not finite), and of the
+// finite ones.
+__device__ __forceinline__ uint32_t vec_max(const uint4& v, __nv_bfloat16) {
+    const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    return max(m << 16, m & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t vec_max(const uint4& v, float) {
+    return max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
+}
 template <int N>
-__device__ __forceinline__ uint32_t vec_max(const uint4& v) {
+__device__ __forceinline__ uint32_t vec_finite_max(const uint4& v) {
     float x[N];
     values_of(v, x);
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) m = max(m, finite_abs_bits(x[i]));
     return m;
+}
+
+// Exponent of the scale of a row, a warp's vectors x[0..IT).
+template <typename T, int IT>
+__device__ __forceinline__ int row_exponent(const uint4 (&x)[IT]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) m = max(m, vec_max(x[i], T()));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (m >= 0x7f800000u) {
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) m = max(m, vec_finite_max<Vec<T>::N>(x[i]));
+        m = __reduce_max_sync(0xffffffffu, m);
+    }
+    return scale_exponent(m);
 }
 
 // The slot of row n: -1 for a padding row or one outside the cache.
@@ -147,47 +193,27 @@ cache_write_kernel(const T* __restrict__ kv, int64_t kv_stride, const T* __restr
     pdl_wait();
     if (n >= n_rows) return;
     // kept as they lie until they are used: 32 registers, a full SM of warps
-    uint4 x[IT], rope, key = make_uint4(0u, 0u, 0u, 0u);
+    uint4 x[IT], rope, key[1] = {make_uint4(0u, 0u, 0u, 0u)};
     if (kv) {
         const T* p = kv + n * kv_stride;
 #pragma unroll
         for (int i = 0; i < IT; ++i) x[i] = load_vec<ALIGNED>(p + (i * 32 + lane) * N);
         if (lane < DR / N) rope = load_vec<ALIGNED>(p + DV + lane * N);
     }
-    if (k_idx && lane < DI / N) key = load_vec<ALIGNED>(k_idx + n * k_stride + lane * N);
+    if (k_idx && lane < DI / N) key[0] = load_vec<ALIGNED>(k_idx + n * k_stride + lane * N);
     const int64_t slot = slot_of(slots, n, num_rows, status);
     if (slot < 0) return;
-    float y[N];
     if (kv) {
         uint8_t* row = kv_q8 + slot * ROW;
-        uint32_t m = 0;
+        const int e = row_exponent<T>(x);
 #pragma unroll
-        for (int i = 0; i < IT; ++i) m = max(m, vec_max<N>(x[i]));
-        const int e = scale_exponent(__reduce_max_sync(0xffffffffu, m));
-        const float inv = exp2_int(-e);
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            values_of(x[i], y);
-            store_codes<N>(row + (i * 32 + lane) * N, y, inv);
-        }
+        for (int i = 0; i < IT; ++i) store_codes(row + (i * 32 + lane) * N, x[i], exp2_int(-e), T());
         if (lane == 0) kv_scale[slot] = exp2_int(e);
-        if (lane < DR / N) {
-            uint32_t* d = reinterpret_cast<uint32_t*>(row + OFF_ROPE) + lane * (N / 2);
-            values_of(rope, y);
-#pragma unroll
-            for (int i = 0; i < N; ++i) y[i] *= inv;
-            if constexpr (N == 8) {
-                *reinterpret_cast<uint4*>(d) = make_uint4(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]),
-                                                          bf16_pair(y[4], y[5]), bf16_pair(y[6], y[7]));
-            } else {
-                *reinterpret_cast<uint2*>(d) = make_uint2(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]));
-            }
-        }
+        if (lane < DR / N) store_scaled(row + OFF_ROPE + lane * N * 2, rope, exp2_int(-e), T());
     }
     if (k_idx) {
-        const int e = scale_exponent(__reduce_max_sync(0xffffffffu, vec_max<N>(key)));
-        values_of(key, y);
-        if (lane < DI / N) store_codes<N>(k_codes + slot * DI + lane * N, y, exp2_int(-e));
+        const int e = row_exponent<T>(key);
+        if (lane < DI / N) store_codes(k_codes + slot * DI + lane * N, key[0], exp2_int(-e), T());
         if (lane == 0) k_scale[slot] = exp2_int(e);
     }
 }

@@ -4,14 +4,18 @@
 // the row format.  For a row x of 512 values (an indexer key: 128)
 //   s = 2^e, e the smallest with max|x| <= 448 * 2^e;  code = e4m3(x / s),
 // and back x' = code * s.  Both directions are bound by memory: a token is
-// 1408 bytes of bfloat16 against 776 bytes of cache.
+// 1408 bytes of bfloat16 against 776 bytes of cache.  Measured on 64K tokens:
+// writing latents and keys 24.6 us (5.8 TB/s, 89 % of a plain copy), reading
+// latents back 22.6 us (5.2 TB/s, 79 %); two tokens a warp read no faster.
 //
 // One warp per token, every load of the token in flight before the first is
 // used; slot and data loads do not wait for one another when writing.  A lane
 // takes the values of one 16-byte vector at a time (8 bfloat16 or 4 float32),
 // so a warp's loads and stores are whole consecutive lines on both sides; the
 // row's maximum is one integer reduction over the warp (non-negative floats
-// order like their bits).
+// order like their bits).  Writing was bound by its arithmetic first: vectors
+// that stay packed until they are used (32 registers, a full SM of warps) took
+// 64K tokens from 36.9 to 28.7 us, packed maxima and products to 24.6.
 #include <algorithm>
 
 #include "q8.cuh"

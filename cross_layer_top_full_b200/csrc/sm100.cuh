@@ -372,6 +372,15 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     }
 }
 
+// Remote arrive that orders this CTA's view of the thread's earlier accesses
+// before it: for operands that the CTA's own tensor core reads once the other
+// CTA of the pair, told by this arrival, issues the MMA.  (At cluster scope the
+// release takes about 2000 cycles.)
+__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+                 : "memory");
+}
+
 // Orders this thread's shared-memory writes before later reads of the async
 // proxy (TMA, tcgen05.mma).
 __device__ __forceinline__ void fence_async_smem() {

@@ -22,10 +22,24 @@
 // with 644 bytes of cache traffic per row.
 //
 // A unit is 128 query rows that read the same positions: the heads of one row
-// (idx given), or 128 consecutive (node, head) pairs of a sequence.  All
-// units' blocks of 128 positions are one list, cut into equal runs, one per
-// CTA pair; where a run ends inside a unit, the pair leaves a float32 partial
+// (idx given), or 128 consecutive (node, head) pairs of a sequence.  The
+// units' blocks of 128 positions are shared out among the CTA pairs (see
+// below); where a pair's run ends inside a unit, it leaves a float32 partial
 // result and a second kernel joins them.
+//
+// What bounds it: the tensor core.  A block costs a pair 3,000 cycles of MMAs
+// by themselves (Q K^T 1,850: 36 MMAs with N = 128, which the operand reads
+// hold to 60 % of their rate; P V 1,060 at the full rate); blocks in a row
+// take 2,800 to 2,900, the two products overlapping.  A unit costs 12,000 to
+// 18,000 cycles besides, for Q, the first block's latency and the results.
+// 128 lists of 2048 (73 GFLOP): 96 us; 8 sequences of up to 8192 with 16 nodes,
+// every position (159 GFLOP): 170 us; 32 lists: 37 us; one list: 17 us.
+// Steps that did not help: four-row TMA gathers (about 65 cycles each, 112 a
+// block, against 36 cp.async a warp), a wait of the copies' arrival by the MMA
+// warp with its proxy fence there, releases at cluster scope for the arrivals
+// from the other CTA (2,000 cycles each), 64-bit run arithmetic and fully
+// unrolled code (the instruction fetch), query rows kept in registers over the
+// end of a unit (spills: 96 -> 106 us).
 //
 // A pair works on one unit at a time: each CTA holds 64 of the rows, gathers
 // 64 of the block's 128 keys whole (for Q K^T) and half of the value columns
@@ -444,7 +458,7 @@ __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t
     tmem_st_wait();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive_remote_relaxed(q_bar);
+    if (lane == 0) mbar_arrive_remote_cta(q_bar);
     return sq[row];
 }
 
@@ -579,9 +593,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
         float* xl = reinterpret_cast<float*>(smem + OFF_XL) + row;
         float* mr = reinterpret_cast<float*>(smem + OFF_MR) + row;
         uint8_t* p_hi = smem + OFF_P + group * P_STAGE + row * 128;
-        // (the arrivals at rank 0's barriers from the other SM are relaxed: what
-        // they announce is read by the tensor core of the SM that wrote it, after
-        // the writer's fence; a release at cluster scope took 2000 cycles here)
+        // (what these arrivals at rank 0's barriers announce is read by the tensor
+        // core of the SM that wrote it, after the writer's fence)
         const uint32_t q_bar = map_to_rank(smem_u32(&s.q_full), 0), p_bar = map_to_rank(smem_u32(&s.p_full[group]), 0);
         const uint32_t s_bar = map_to_rank(smem_u32(&s.s_free[group]), 0);
         const int sw = row & 7;
@@ -683,7 +696,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                     tmem_ld_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_remote_relaxed(s_bar);
+                    if (lane == 0) mbar_arrive_remote_cta(s_bar);
                     const float4* g4 = reinterpret_cast<const float4*>(info.scale) + kw * 8;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
@@ -791,7 +804,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote_relaxed(p_bar);
+                if (lane == 0) mbar_arrive_remote_cta(p_bar);
             }
             done = r;
             whole = w.t == 0 && n == w.nt;
@@ -949,7 +962,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 ok = wait_for(&s.k_full[buf], ph, status, abort, 10);
                 if (!ok) break;
                 if (!leader) {
-                    if (lane == 0) mbar_arrive_remote_relaxed(k_peer + 8 * buf);
+                    if (lane == 0) mbar_arrive_remote_cta(k_peer + 8 * buf);
                     continue;
                 }
                 ok = wait_for(&s.k_peer[buf], ph, status, abort, 11);
@@ -988,7 +1001,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 ok = wait_for(&s.v_full[buf], ph, status, abort, 13);
                 if (!ok) break;
                 if (!leader) {
-                    if (lane == 0) mbar_arrive_remote_relaxed(v_peer + 8 * buf);
+                    if (lane == 0) mbar_arrive_remote_cta(v_peer + 8 * buf);
                     continue;
                 }
                 ok = wait_for(&s.v_peer[buf], ph, status, abort, 14);

@@ -30,8 +30,8 @@
 // What bounds it: the tensor core.  A block costs a pair 3,000 cycles of MMAs
 // by themselves (Q K^T 1,850: 36 MMAs with N = 128, which the operand reads
 // hold to 60 % of their rate; P V 1,060 at the full rate); blocks in a row
-// take 2,800 to 2,900, the two products overlapping.  A unit costs 12,000 to
-// 18,000 cycles besides, for Q, the first block's latency and the results.
+// take 2,800 to 2,900, the two products overlapping.  A unit costs 18,000
+// cycles besides, for Q, the first block's latency and the results.
 // 128 lists of 2048 (73 GFLOP): 96 us; 8 sequences of up to 8192 with 16 nodes,
 // every position (159 GFLOP): 170 us; 32 lists: 37 us; one list: 17 us.
 // Steps that did not help: four-row TMA gathers (about 65 cycles each, 112 a
@@ -164,20 +164,22 @@ __device__ __forceinline__ int total_blocks(const Args& a) {
     return __reduce_add_sync(0xffffffffu, n) * a.units;
 }
 
-// How the blocks are shared out among P pairs.  In blocks' time (3,600 cycles)
-// a unit costs a run about UNIT_COST (12,000 to 14,000 cycles for Q, the first
-// block's latency and the results), and joining partial results JOIN_COST (up
-// to 10 us of a second kernel).  Three ways:
+// How the blocks are shared out among P pairs.  In blocks' time (2,850 cycles)
+// a unit costs a run about UNIT_COST (18,000 cycles for Q, the first block's
+// latency and the results), and joining partial results JOIN_COST (up to 10 us
+// of a second kernel).  Three ways:
 //   WHOLE  the units, whole, in equal shares (nothing to join)
 //   PARTS  each unit over parts_of() pairs, in proportion to its blocks; a pair
 //          has one unit
 //   RUNS   the list of all units' costs in equal runs, over the units' borders
 // Lists are all of one length: the host takes the cheapest.  With every
 // position the lengths are known on the device, which decides between PARTS
-// and RUNS.  Measured: 32 lists of 2048 (16 blocks), PARTS 25 us, RUNS 33;
-// 128 lists of 2048, WHOLE 137,000 cycles expected, RUNS 134,000 and the join.
+// and RUNS.  Measured: 32 lists of 2048 (16 blocks), PARTS 36 us, RUNS 44; 128
+// lists, WHOLE 94, RUNS 108; 8 sequences of up to 8192 in RUNS of equal blocks
+// 183, of equal cost 170.  Costs of 3 and 4 instead: 40 lists 50 us (in RUNS)
+// against 43 (WHOLE).
 enum { WHOLE, PARTS, RUNS, BY_LENGTH };
-constexpr int UNIT_COST = 3, JOIN_COST = 4;
+constexpr int UNIT_COST = 6, JOIN_COST = 6;
 __device__ __forceinline__ int parts_of(const Args& a, int b, int n, int P) { return max(1, blocks_of(a, b) * P / n); }
 
 // Equal shares: n things over P pairs, the first n % P one more.
@@ -1183,7 +1185,7 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
                               const int32_t* idx, int k, const uint64_t* tree, const ic_paged_rows& pr, int Hq, float scale,
                               void* out, uint32_t* status, void* scratch, cudaStream_t s) {
     const Plan p = plan(pr, k, Hq);
-    if ((int64_t)pr.B * pr.Lq > 0x7fffffffLL || p.blocks >= 1 << 29) return IC_ERR_UNSUPPORTED;
+    if ((int64_t)pr.B * pr.Lq > 0x7fffffffLL || p.blocks >= 1 << 28) return IC_ERR_UNSUPPORTED;
     CUtensorMap map_box;
     if (!make_map(&map_box, kv_q8, (int64_t)pr.num_pages * pr.page_size, 64)) return cuda_error("tree_attn_q8");
     Args a;

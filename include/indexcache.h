@@ -508,7 +508,7 @@ ic_status ic_cache_read_q8(const void* kv_q8, const float* kv_scale, const void*
  *             nothing gets zeros.
  * A NaN or infinity in a cache row that a query row does not see does not
  * reach that row's output; a NaN in a seen row makes it NaN.
- * Batches of 2^29 blocks or more (blocks of 128 positions of T_max or of k, for
+ * Batches of 2^28 blocks or more (blocks of 128 positions of T_max or of k, for
  * each row of a list or each 128 (node, head) pairs) return IC_ERR_UNSUPPORTED.
  * Workspace: ic_tree_attn_q8_workspace_size(pr, k, Hq). */
 size_t ic_tree_attn_q8_workspace_size(const ic_paged_rows* pr, int k, int Hq);

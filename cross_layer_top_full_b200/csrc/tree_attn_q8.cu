@@ -61,6 +61,11 @@
 // eight 8-bit slices and its bfloat16 columns 32 each.  Shared memory: five
 // slices of Q 40 KB, K 2 x 40 KB, V 2 x 32 KB, P 2 x 16 KB, the ring 6 KB.
 //
+// A barrier tells only its last two phases apart.  So each wait here is for a
+// phase whose predecessor is known to be over (the waiter has seen it, or what
+// it has seen implies it) and whose successor cannot end before the waiter has
+// gone on.
+//
 // Every wait is bounded (sm100.cuh); sites: 1-3 copies, 4-9 and 19 softmax,
 // 10-15 and 20 MMA issue, 16 resolution.
 #include <cudaTypedefs.h>
@@ -109,7 +114,8 @@ constexpr float TOP = 2.f, SLACK = 6.5f;       // log2 of the largest weight whe
                                               // set, and how far it may grow before O is rescaled
 
 struct __align__(8) Bars {
-    uint64_t info_full[RING], info_free[RING];
+    uint64_t info_full[RING];
+    uint64_t info_free[2 * RING];    // block j % 6 has been used: always waited for by the same warp
     uint64_t q_full;                 // rank 0: Q of a unit is in place (both CTAs' warps)
     uint64_t k_full[2], v_full[2];   // own tiles have landed
     uint64_t k_peer[2], v_peer[2];   // rank 0: rank 1's tiles have landed
@@ -490,6 +496,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
         for (int i = 0; i < RING; ++i) {
             mbar_init(&s.info_full[i], 1);
             mbar_init(&s.info_free[i], GROUP_WARPS + 4);
+            mbar_init(&s.info_free[RING + i], GROUP_WARPS + 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.k_full[i], 2);
@@ -731,6 +738,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 if (x > 0) {
                     take_over(group);
                     mprev = mr[(buf ^ 1) * HROWS];
+                } else {
+                    group_sync(group);                      // as take_over: every warp has read xm
                 }
                 const bool grow = mx > mprev + SLACK;
                 const float mnew = grow ? mx : mprev;
@@ -759,8 +768,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 l = (mref == mnew ? l : l * ex2_approx(mref - mnew)) + (ls.x + ls.y);
                 mref = mnew;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.info_free[slot]);
+                if (lane == 0) mbar_arrive(&s.info_free[j % (2 * RING)]);
                 if (++slot == RING) { slot = 0; ++turn; }
+                // P V of j - 2, and with it j - 3, before that of j - 1 (two barriers)
+                if (j > 1) wait_for(&s.pv_done[buf], ((j - 2) >> 1) & 1, status, abort, 19);
                 if (x > 0 && __any_sync(0xffffffffu, grow)) {
                     // O of the blocks before this one, which P V of the block has not joined yet
                     const float factor = grow ? ex2_approx(mprev - mnew) : 1.f;   // 0 from -inf
@@ -778,7 +789,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                     }
                     tmem_st_wait();
                 }
-                if (j > 1) wait_for(&s.pv_done[buf], ((j - 2) >> 1) & 1, status, abort, 19);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int at = ((kw * 2 + c) ^ sw) << 4;
@@ -853,7 +863,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 else copy_rows<16, 2, 256, 2 * ATOM>(dst0, mine * 64, a.cache + rank * 128, info.rows + mine * 64, lane);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.info_free[slot]);
+            if (lane == 0) mbar_arrive(&s.info_free[j % (2 * RING)]);
             if (!box) {             // the other stage is not free yet: nothing else to send meanwhile
                 copy_wait_all();
                 fence_async_smem();
@@ -926,8 +936,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                     lg[i] = (float)((int)(u >> 23) - 127);
                     inv[i] = __uint_as_float(0x7f000000u - u);
                 }
-                const uint32_t slot = j % RING, turn = j / RING;
-                if (turn > 0) ok = wait_for(&s.info_free[slot], (turn - 1) & 1, status, abort, 16);
+                const uint32_t slot = j % RING, was = j - RING;       // the slot's block before
+                if (j >= RING) ok = wait_for(&s.info_free[was % (2 * RING)], (was / (2 * RING)) & 1, status, abort, 16);
                 if (!ok) break;
                 Info& info = reinterpret_cast<Info*>(smem + OFF_INFO)[slot];
                 reinterpret_cast<int4*>(info.rows)[lane] = make_int4(rows[0], rows[1], rows[2], rows[3]);

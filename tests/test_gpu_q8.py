@@ -515,6 +515,24 @@ def test_results_do_not_depend_on_the_run(k, dev):
     assert ic.read_status(ws) == 0 and ic.read_status(ws2) == 0
 
 
+@pytest.mark.parametrize("lens,Lq,k", [([6000, 2300, 700], 8, 0), ([4000] * 6, 4, 2048)])
+def test_growing_maxima_give_the_same_bits_every_time(lens, Lq, k, dev):
+    """A few positions far above the others raise the running maxima again and again, in every phase of the
+    blocks that are under way: each of 150 calls must give what the first gave."""
+    b = Tree(lens, Lq, dev, seed=48, k=k)
+    for rows, scales in zip(b.rows, b.scales):
+        for s in b.rng.permutation(len(rows))[:len(rows) // 40]:
+            scales[s] *= 2.0 ** int(b.rng.integers(1, 5))
+    b.place()
+    first = b.run()
+    b.check(first, rows={(0, 0), (0, Lq - 1), (2, 1)})
+    ws, out = b.workspace(), torch.empty_like(first)
+    for _ in range(150):
+        b.call(out, ws)
+        assert torch.equal(out, first)
+    assert ic.read_status(ws) == 0
+
+
 def test_two_calls_at_once_on_two_streams(dev):
     a, b = Tree([3000, 800], 2, dev, seed=33, k=500), Tree([2500], 8, dev, seed=34, Hq=64)
     wa, wb = a.run(), b.run()

@@ -17,7 +17,10 @@
 //     weight, 3 down to 2^-16, so that many small weights beside a large one
 //     are not lost.  The running maximum is that of log2 w_s, which keeps w
 //     in 8-bit range whatever the scales are; the largest weight stands
-//     between 2^2 and 2^8.5.  The softmax sum adds w_s / g_s in float32.
+//     between 2^2 and 2^8.5.  The softmax sum adds w_s / g_s in float32,
+//     before that rounding: with the rounded weights a sharp row comes closer
+//     (at worst 3.3 instead of 4.5e-3 off), but 40,000 small weights beside a
+//     large one, rounded down together, take the row 8e-3 off instead of 1e-3.
 // Two 8-bit products cost what one of bfloat16 does, without the decoding and
 // with 644 bytes of cache traffic per row.
 //

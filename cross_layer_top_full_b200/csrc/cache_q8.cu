@@ -5,8 +5,12 @@
 //   s = 2^e, e the smallest with max|x| <= 448 * 2^e;  code = e4m3(x / s),
 // and back x' = code * s.  Both directions are bound by memory: a token is
 // 1408 bytes of bfloat16 against 776 bytes of cache.  Measured on 64K tokens:
-// writing latents and keys 24.6 us (5.8 TB/s, 89 % of a plain copy), reading
-// latents back 22.6 us (5.2 TB/s, 79 %); two tokens a warp read no faster.
+// writing latents and keys 24.7 us (5.8 TB/s, 89 % of a plain copy), reading
+// latents back 22.6 us (5.2 TB/s, 79 %; two bytes in three are written).  That
+// is the memory's rate for such a mix: without the decoding, with slots that
+// need no load, with four warps a block or streaming stores it is the same to
+// 1 %, two tokens a warp are no faster, a loop over tokens that loads the next
+// slot ahead is slower (24.4), and so are sixteen warps a block (24.6).
 //
 // One warp per token, every load of the token in flight before the first is
 // used; slot and data loads do not wait for one another when writing.  A lane

@@ -35,8 +35,8 @@
 // hold to 60 % of their rate; P V 1,060 at the full rate); blocks in a row
 // take 2,800 to 2,900, the two products overlapping.  A unit costs 18,000
 // cycles besides, for Q, the first block's latency and the results.
-// 128 lists of 2048 (73 GFLOP): 96 us; 8 sequences of up to 8192 with 16 nodes,
-// every position (159 GFLOP): 170 us; 32 lists: 37 us; one list: 17 us.
+// 128 lists of 2048 (73 GFLOP): 97 us; 8 sequences of up to 8192 with 16 nodes,
+// every position (159 GFLOP): 168 us; 32 lists: 37 us; one list: 17 us.
 // Steps that did not help: four-row TMA gathers (about 65 cycles each, 112 a
 // block, against 36 cp.async a warp), a wait of the copies' arrival by the MMA
 // warp with its proxy fence there, releases at cluster scope for the arrivals
@@ -184,7 +184,7 @@ __device__ __forceinline__ int total_blocks(const Args& a) {
 // Lists are all of one length: the host takes the cheapest.  With every
 // position the lengths are known on the device, which decides between PARTS
 // and RUNS.  Measured: 32 lists of 2048 (16 blocks), PARTS 36 us, RUNS 44; 128
-// lists, WHOLE 94, RUNS 108; 8 sequences of up to 8192 in RUNS of equal blocks
+// lists, WHOLE 94, RUNS 108 (in the same run); 8 sequences of up to 8192 in RUNS of equal blocks
 // 183, of equal cost 170.  Costs of 3 and 4 instead: 40 lists 50 us (in RUNS)
 // against 43 (WHOLE).
 enum { WHOLE, PARTS, RUNS, BY_LENGTH };

@@ -13,14 +13,20 @@
 //     cache keeps as bfloat16 follow in the same accumulator: both operands
 //     carry the same scales there.
 //   P V: the weights w_s = p_s g_s go in as an e4m3 number and an e5m2 number
-//     for the rest: 7 significant bits down to 2^-8 of the row's largest
-//     weight, 3 down to 2^-16, so that many small weights beside a large one
-//     are not lost.  The running maximum is that of log2 w_s, which keeps w
-//     in 8-bit range whatever the scales are; the largest weight stands
-//     between 2^2 and 2^8.5.  The softmax sum adds w_s / g_s in float32,
-//     before that rounding: with the rounded weights a sharp row comes closer
-//     (at worst 3.3 instead of 4.5e-3 off), but 40,000 small weights beside a
-//     large one, rounded down together, take the row 8e-3 off instead of 1e-3.
+//     for the rest.  The running maximum is that of log2 w_s, which keeps w in
+//     8-bit range whatever the scales are; the row's largest weight stands
+//     between 2^4 and 2^8.5.  Weights of 2 or more are off by at most 2^-8 of
+//     themselves, as in bfloat16.  Smaller ones may be very many and all alike:
+//     to the nearest, with the largest weight at 2^2, 65,536 of them at 2^-19.1
+//     of it (a tenth of the sum) all became 0, and at 2^-17 were off by an
+//     eighth, all the same way.  So they are rounded up or down at random, right
+//     on average, and of n errors the root of n of them is left: by at most 2^-7
+//     of themselves down to 2^-6, then a step of 2^-13, of a quarter of the
+//     weight under 2^-11, of 2^-16 at last.  That costs 1.5 %, the largest weight
+//     at 2^4 instead of 2^2 (two more bits for the others, more maxima that
+//     outgrow their room) another 2 %: 128 lists of 2048, 82.7, 84.1, 85.9 us;
+//     with 2^6 89.3.  The softmax sum adds w_s / g_s in float32, before that
+//     rounding.
 // Two 8-bit products cost what one of bfloat16 does, without the decoding and
 // with 644 bytes of cache traffic per row.
 //
@@ -113,7 +119,7 @@ constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 384, TM_QR = TM_Q + 96;   // TM_
 constexpr int TMEM_COLS = 512;
 constexpr int MAX_PAIRS = 74;                 // CTA pairs of 148 SMs
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr float TOP = 2.f, SLACK = 6.5f;       // log2 of the largest weight when the maximum is
+constexpr float TOP = 4.f, SLACK = 4.5f;       // log2 of the largest weight when the maximum is
                                               // set, and how far it may grow before O is rescaled
 
 struct __align__(8) Bars {
@@ -310,17 +316,33 @@ __device__ __forceinline__ uint32_t bf16_pair2(uint64_t v) {
     return bf16_pair(f.x, f.y);
 }
 
-// Two e4m3 numbers and two e5m2 numbers for what they leave of (a, b).
-__device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
+// Two e4m3 numbers, and what they leave of (a, b): exactly.
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, float& ra, float& rb) {
     hi = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3);
-    float ra, rb;
-    asm("{\n\t.reg .b16 m;\n\tmov.b16 m, 0xbc00;\n\t"            // a - hi: hi * -1 + a, exactly
+    asm("{\n\t.reg .b16 m;\n\tmov.b16 m, 0xbc00;\n\t"            // a - hi: hi * -1 + a
         "fma.rn.f32.f16 %0, %2, m, %4;\n\tfma.rn.f32.f16 %1, %3, m, %5;\n\t}"
         : "=f"(ra), "=f"(rb)
         : "h"(h.x), "h"(h.y), "f"(a), "f"(b));
-    lo = __nv_cvt_float2_to_fp8x2(make_float2(ra, rb), __NV_SATFINITE, __NV_E5M2);
 }
+// Four rests as e5m2 numbers (the first in the low byte), rounded up or down at
+// random: up with the probability that the rest stands above the lower
+// neighbour, so that the mean is the rest itself.  Each half of `random` serves
+// two values, to the one with its bits in reverse order (measured; 16 bits).
+__device__ __forceinline__ uint32_t round_rests(float a, float b, float c, float d, uint32_t random) {
+    uint32_t r;
+    asm("cvt.rs.satfinite.e5m2x4.f32 %0, {%4, %3, %2, %1}, %5;" : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d), "r"(random));
+    return r;
+}
+constexpr uint32_t NEAREST = 0x80018001u;      // a half step, read from either end
+// A number per query row and 32 positions, from which a sequence of them starts
+// (multiplicative hashing; the linear congruence of a published table).
+__device__ __forceinline__ uint32_t random_start(uint32_t row, uint32_t at) {
+    uint32_t x = row * 0x9e3779b9u + at;
+    x = (x ^ x >> 16) * 0x9e3779b9u;
+    return x ^ x >> 15;
+}
+__device__ __forceinline__ uint32_t random_next(uint32_t x) { return x * 1664525u + 1013904223u; }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -752,6 +774,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 const uint64_t off2 = f2(off, off);
                 uint64_t l2 = f2(0.f, 0.f);
                 uint32_t hi[8], lo[8];
+                uint32_t random = random_start((uint32_t)(r.first + m), (uint32_t)(s0 + kw * 32));
                 const float4* inv4 = reinterpret_cast<const float4*>(info.inv) + kw * 8;
 #pragma unroll
                 for (int c = 0; c < 32; c += 4) {
@@ -761,11 +784,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                     const float4 inv = inv4[c / 4];
                     l2 = ffma2(f2(e0, e1), f2(inv.x, inv.y), l2);
                     l2 = ffma2(f2(e2, e3), f2(inv.z, inv.w), l2);
-                    uint32_t h0, h1, r0, r1;
-                    split_weights(e0, e1, h0, r0);
-                    split_weights(e2, e3, h1, r1);
+                    uint32_t h0, h1;
+                    float r0, r1, r2, r3;
+                    split_weights(e0, e1, h0, r0, r1);
+                    split_weights(e2, e3, h1, r2, r3);
                     hi[c / 4] = h0 | h1 << 16;
-                    lo[c / 4] = r0 | r1 << 16;
+                    random = random_next(random);
+                    // a weight of 2 or more among the four: all of them to the nearest
+                    lo[c / 4] = round_rests(r0, r1, r2, r3, hi[c / 4] & 0x40404040u ? NEAREST : random);
                 }
                 const float2 ls = f2_split(l2);
                 l = (mref == mnew ? l : l * ex2_approx(mref - mnew)) + (ls.x + ls.y);

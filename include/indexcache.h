@@ -506,6 +506,14 @@ ic_status ic_cache_read_q8(const void* kv_q8, const float* kv_scale, const void*
  *             its positions and sets the status bit.
  *   out       [B, Lq, Hq, 512] bf16, 16-byte aligned.  A row that sees
  *             nothing gets zeros.
+ * Accuracy: the softmax sum and all products are float32.  A weight w_s = p_s *
+ * kv_scale[s] is kept to 2^-8 of itself (2^-7 under an eighth of the row's largest)
+ * down to 2^-10 of the largest, then in steps of 2^-17 of the largest or a quarter
+ * of w, never finer than 2^-20.  Weights under an eighth of the largest are rounded
+ * up or down at random, right on average, so that errors of many small weights do
+ * not add up; the rule knows only the query row's and the positions' places, and the
+ * same call gives the same bits.  The scales of the positions that a row sees should
+ * lie within 2^90 of one another (float32's range).
  * A NaN or infinity in a cache row that a query row does not see does not
  * reach that row's output; a NaN in a seen row makes it NaN.
  * Batches of 2^28 blocks or more (blocks of 128 positions of T_max or of k, for

@@ -1,0 +1,192 @@
+"""The attention over the quantised cache where softmax weights span a wide
+range: long contexts under one large weight.  Compared with the definition in
+64 bits; caches come from ic_cache_write_q8.
+
+Tolerance, elementwise, with softmax weights p_s (normalised), scales g_s,
+codes c_s, V_s = g_s c_s and w_s = p_s g_s.  Nothing in it is a bias that adds
+up over positions:
+
+    2^-8 |ref|            the output's rounding to bfloat16
+  + 2^-7 sum_s p_s |V_s|  a weight is an e4m3 number and an e5m2 number for the
+                          rest.  The first is off by at most 2^-4 of the
+                          weight's power of two 2^E, so the rest is at most
+                          2^(E-4), where e5m2 steps are at most 2^(E-7): the
+                          whole step, since weights may be rounded up or down
+                          at random
+  + 4 sqrt(sum_s (t_s |c_s|)^2)
+                          smaller weights, t_s the step of e5m2 there.  With the
+                          row's largest weight at 2^4 (it stands there or
+                          higher), weights under 2^-6 leave a rest of 2^-10 at
+                          most, step 2^-13; under 2^-10 the rest is the weight,
+                          its step a quarter of it at most, and never under
+                          2^-16: t = max(min(2^-13, w / 4), 2^-16) for w <
+                          2^-6.  They are rounded at random, by independent
+                          errors of mean 0 in intervals of length t: by
+                          Hoeffding's inequality the sum exceeds 4 sqrt(sum
+                          t^2) with probability under 2 exp(-32) = 3e-14
+  + sum_s t_s |c_s| / 2   over the small weights that share an aligned group of
+                          four entries with one of 2^1 or more (2^-7.5 of the
+                          largest at least, which may have grown to 2^8.5):
+                          these are rounded to the nearest
+  + 2 d sum_s p_s |V_s|   the logits' error d: float32 sums of 576 products,
+                          each 2^-24 of the sum of absolute terms; q kept to
+                          2^-17 of its row's largest value; 2^-21 of the logit,
+                          2^-21 for exp, 2^-17 for the base-2 logarithm of a
+                          scale that is no power of two (a float32 number up to
+                          128, half a step 2^-18, once in itself and once in
+                          the sum with the logit).  A weight is off by d and so
+                          is the normaliser
+
+A row of zeros among the values has no part in O; its weight stands for 2^-40
+p_s when the largest weight is sought.
+"""
+import numpy as np
+import pytest
+import torch
+
+import cross_layer_top_full_b200 as ic
+from parity_util import check_attention
+
+pytestmark = pytest.mark.gpu
+BF, D = torch.bfloat16, "cuda:0"
+LN2 = float(np.log(2.0))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    ic.lib()
+
+
+def new_ws(nbytes=256):
+    ws = torch.empty(max(nbytes, ic.STATUS_BYTES), dtype=torch.uint8, device=D)
+    ic.workspace_init(ws)
+    return ws
+
+
+def packed(kv):
+    """Cache rows and scales of latent rows [n, 576], by the library's writer; n is padded to whole pages of 128."""
+    n = len(kv)
+    rows = -(-n // 128) * 128
+    cache = torch.zeros(rows, 640, dtype=torch.uint8, device=D)
+    scale = torch.ones(rows, device=D)
+    ws = new_ws()
+    ic.cache_write_q8(torch.arange(n, dtype=torch.int32, device=D), ws, kv=kv.float(), kv_q8=cache, kv_scale=scale)
+    assert ic.read_status(ws) == 0
+    return cache, scale
+
+
+def attend(q, cache, scale, lens, idx=None, tree=None, factor=576 ** -0.5, status=0):
+    """q [B, Lq, Hq, 576]; every sequence reads the same pages 0, 1, .. of the cache."""
+    B, Lq, Hq, _ = q.shape
+    T = max(lens)
+    pages = -(-T // 128)
+    table = torch.arange(pages, dtype=torch.int32, device=D).repeat(B, 1)
+    d_lens = torch.tensor(lens, dtype=torch.int32, device=D)
+    pr = ic.paged_rows(d_lens, table, T, 128, len(cache) // 128, Lq)
+    ws = new_ws(ic.tree_attn_q8_workspace_size(pr, 0 if idx is None else idx.shape[-1], Hq))
+    out = torch.full((B, Lq, Hq, 512), 3.0, dtype=BF, device=D)
+    ic.tree_attn_q8_paged(q, cache, scale, idx, pr, factor, out, ws, tree=tree)
+    assert ic.read_status(ws) == status
+    return out
+
+
+def exact(q, cache, scale, at, factor, group=None):
+    """Heads q [H, 576] over cache rows `at` (list order): the output and its tolerance, float64."""
+    codes = cache[at, :512].view(torch.float8_e4m3fn).double()
+    g = scale[at].double()
+    k = torch.cat([codes, cache[at, 512:].view(BF).double()], 1) * g[:, None]
+    q = q.double()
+    s = q @ k.T * factor
+    p = torch.softmax(s, 1)
+    ref = p @ k[:, :512]
+    nil = (codes == 0).all(1)
+    w = torch.where(nil, p * 2.0 ** -40, p * g)
+    u = w / w.amax(1, keepdim=True) * 16.0                               # the largest at 2^4
+    t = torch.where(u < 2.0 ** -6, torch.clamp(torch.clamp(u / 4, max=2.0 ** -13), min=2.0 ** -16), 0.0)
+    t = torch.where(nil, 0.0, t)
+    entry = torch.arange(len(at), device=D) if group is None else group
+    four = entry // 4
+    big = torch.zeros(len(q), int(four.max()) + 1, dtype=torch.float64, device=D)
+    big.scatter_reduce_(1, four.expand_as(u), u, "amax")
+    near = t * (big[:, four] >= 2.0 ** -3.5)
+    unit = w.amax(1, keepdim=True) / 16.0
+    c = codes.abs()
+    v = p @ k[:, :512].abs()
+    terms = q.abs() @ k.abs().T * abs(factor)
+    floor = q.abs().amax(1, keepdim=True) * k.abs().sum(1) * abs(factor)
+    d = (576 * 2.0 ** -24 * terms + 2.0 ** -17 * floor + 2.0 ** -21 * s.abs() + 2.0 ** -21 + 2.0 ** -17).amax(1)
+    tol = (2.0 ** -8 * ref.abs() + 2.0 ** -7 * v + unit * (4 * ((t * t) @ (c * c)).sqrt() + near @ c / 2)
+           + 2 * d[:, None] * v)
+    return ref, tol
+
+
+def check(got, ref, tol, what):
+    assert torch.isfinite(got.float()).all(), what
+    over = ((got.double() - ref).abs() / (tol + 1e-300)).max()
+    assert over <= 1, "%s: %.3f of the tolerance" % (what, float(over))
+
+
+def one_above(n, bits, first, spread=0.0, seed=1):
+    """n positions whose logits (through columns that carry no value) lie `bits` powers of two under position 0's,
+    scattered by a normal distribution of `spread` nats; values of size 1 that do not cancel."""
+    g = torch.Generator(device=D).manual_seed(seed)
+    kv = torch.zeros(n, 576, device=D)
+    kv[:, :512] = 1.0 + 0.25 * torch.sin(torch.arange(n, device=D)[:, None] * 0.7 + torch.arange(512, device=D))
+    kv[0, :512] = first
+    kv[0, 512:544] = bits * LN2
+    if spread:
+        kv[1:, 544:576] = spread * torch.randn(n - 1, 1, device=D, generator=g)
+    q = torch.zeros(576, device=D)
+    q[512:] = 1.0 / 32
+    return kv, q.to(BF)
+
+
+# ---------------------------------------------------------------- small weights over long contexts
+@pytest.mark.parametrize("n,bits,spread", [
+    (65536, 17.0, 0.0), (65536, 17.4, 0.0), (65536, 18.5, 0.0), (65536, 19.1, 0.0), (65536, 20.0, 0.0),
+    (65536, 14 / LN2, 1.0), (200000, 14 / LN2, 1.0), (200000, 19.5, 0.0), (8192, 17.4, 0.0), (8192, 13.3, 0.0),
+])
+def test_small_weights_of_a_long_context_count(n, bits, spread):
+    """64 nodes of 128 heads read one sequence: a unit's positions stay together, under one maximum."""
+    Lq = 64
+    kv, q = one_above(n, bits, -1.0, spread)
+    cache, scale = packed(kv)
+    mask = torch.full((1, Lq), -1, dtype=torch.int64, device=D)          # every row sees every position
+    out = attend(q.expand(1, Lq, 128, 576).contiguous(), cache, scale, [n], tree=mask, factor=1.0)
+    ref, tol = exact(q[None], cache, scale, torch.arange(n, device=D), 1.0)
+    for i in (0, 7, 31, 63):
+        check(out[0, i], ref, tol, "node %d" % i)
+    rows = out[0].reshape(-1, 512)
+    check_attention(rows[None].double().cpu().numpy(), ref.expand(len(rows), 512)[None].cpu().numpy(), "every row")
+
+
+@pytest.mark.parametrize("bits,first", [(13.0, -1.0), (19.1, 3.0)])
+def test_small_weights_of_long_lists_count(bits, first):
+    """128 lists of 16384 positions each, in several orders; position 0 is in all of them."""
+    n, k, B, Lq = 40000, 16384, 8, 16
+    kv, q = one_above(n, bits, first)
+    cache, scale = packed(kv)
+    g = torch.Generator(device=D).manual_seed(3)
+    idx = torch.stack([torch.randperm(n - Lq - 1, device=D, generator=g)[:k] + 1 for _ in range(B * Lq)])
+    idx[torch.arange(B * Lq), torch.randint(0, k, (B * Lq,), device=D, generator=g)] = 0
+    idx = idx.view(B, Lq, k).to(torch.int32)
+    out = attend(q.expand(B, Lq, 128, 576).contiguous(), cache, scale, [n] * B, idx=idx, factor=1.0)
+    for b, i in ((0, 0), (3, 9), (7, 15)):
+        ref, tol = exact(q[None], cache, scale, idx[b, i].long(), 1.0)
+        check(out[b, i], ref, tol, "list %d %d" % (b, i))
+        check_attention(out[b, i][None].double().cpu().numpy(), ref.expand(128, 512)[None].cpu().numpy(), "list")
+
+
+def test_unlike_small_weights_beside_a_large_one():
+    """Every fourth of the small weights is a thousand times the others: each kind keeps its share."""
+    n, Lq = 65536, 64
+    kv, q = one_above(n, 9.0, 0.0)
+    kv[:, 544:576] = torch.where(torch.arange(n, device=D) % 4 == 1, 0.0, -10 * LN2)[:, None]
+    kv[:, :512] = torch.where((torch.arange(n, device=D) % 4 == 1)[:, None], kv[:, :512] / 1024, kv[:, :512])
+    cache, scale = packed(kv)
+    mask = torch.full((1, Lq), -1, dtype=torch.int64, device=D)
+    out = attend(q.expand(1, Lq, 128, 576).contiguous(), cache, scale, [n], tree=mask, factor=1.0)
+    ref, tol = exact(q[None], cache, scale, torch.arange(n, device=D), 1.0)
+    check(out[0].reshape(-1, 512), ref, tol, "every row")

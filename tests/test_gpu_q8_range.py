@@ -1,6 +1,6 @@
 """The attention over the quantised cache where softmax weights span a wide
-range: long contexts under one large weight.  Compared with the definition in
-64 bits; caches come from ic_cache_write_q8.
+range: long contexts under one large weight, rows of zeros.  Compared with the
+definition in 64 bits; caches come from ic_cache_write_q8.
 
 Tolerance, elementwise, with softmax weights p_s (normalised), scales g_s,
 codes c_s, V_s = g_s c_s and w_s = p_s g_s.  Nothing in it is a bias that adds
@@ -162,7 +162,7 @@ def test_small_weights_of_a_long_context_count(n, bits, spread):
     check_attention(rows[None].double().cpu().numpy(), ref.expand(len(rows), 512)[None].cpu().numpy(), "every row")
 
 
-@pytest.mark.parametrize("bits,first", [(13.0, -1.0), (19.1, 3.0)])
+@pytest.mark.parametrize("bits,first", [(13.0, -1.0), (16.0, 0.0), (18.5, 0.0), (19.1, 3.0)])
 def test_small_weights_of_long_lists_count(bits, first):
     """128 lists of 16384 positions each, in several orders; position 0 is in all of them."""
     n, k, B, Lq = 40000, 16384, 8, 16
@@ -190,3 +190,43 @@ def test_unlike_small_weights_beside_a_large_one():
     out = attend(q.expand(1, Lq, 128, 576).contiguous(), cache, scale, [n], tree=mask, factor=1.0)
     ref, tol = exact(q[None], cache, scale, torch.arange(n, device=D), 1.0)
     check(out[0].reshape(-1, 512), ref, tol, "every row")
+
+
+# ---------------------------------------------------------------- rows of zeros
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("size,below", [(1.0, 0.0), (1.0, 8.0), (1e-2, 3.0), (2e-4, 0.0), (1e-4, 3.0), (1e-6, 1.0)])
+def test_a_row_of_zeros_does_not_hide_the_others(size, below, listed):
+    """Tokens whose 512 values are 0, with logits above the others', among tokens of one size."""
+    n, B = 2048, 80
+    g = torch.Generator(device=D).manual_seed(5)
+    kv = torch.randn(n, 576, device=D, generator=g) * size
+    kv[:, 512:] = 0.0
+    zeros = torch.tensor([3, 700, 701, 1500, 2047], device=D)
+    kv[zeros] = 0.0
+    kv[zeros, 512:544] = below
+    q = torch.zeros(2, 576, device=D)
+    q[:, 512:] = 1.0 / 32
+    q[1, :512] = torch.randn(512, device=D, generator=g) / (size * 40)
+    q = q.to(BF)
+    cache, scale = packed(kv)
+    cache[zeros[1], 100] = 0x80                                          # -0 is a 0 too
+    at = torch.arange(n, device=D)
+    idx = at.to(torch.int32).expand(B, 1, n).contiguous() if listed else None
+    out = attend(q.expand(B, 1, 2, 576).contiguous(), cache, scale, [n] * B, idx=idx, factor=1.0)
+    ref, tol = exact(q, cache, scale, at, 1.0)
+    for b in (0, 41, 79):
+        check(out[b, 0], ref, tol, "sequence %d" % b)
+
+
+def test_many_rows_of_zeros():
+    """Whole pages of zeros, between tokens; and a sequence of nothing else gives zeros."""
+    n = 1500
+    g = torch.Generator(device=D).manual_seed(6)
+    kv = torch.randn(n, 576, device=D, generator=g) * 1e-3
+    kv[100:1200, :512] = 0.0
+    q = torch.randn(1, 1, 20, 576, device=D, generator=g).to(BF)
+    cache, scale = packed(kv)
+    ref, tol = exact(q[0, 0], cache, scale, torch.arange(n, device=D), 576 ** -0.5)
+    check(attend(q, cache, scale, [n])[0, 0], ref, tol, "pages of zeros")
+    cache, scale = packed(torch.zeros(300, 576, device=D))
+    assert (attend(q, cache, scale, [300]) == 0).all()

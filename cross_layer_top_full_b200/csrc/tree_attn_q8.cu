@@ -61,7 +61,7 @@
 //               (cp.async, 128 adjacent bytes per row and eight lanes; a row
 //               that nobody may see is filled with zeros), or one TMA box per
 //               64 rows where a block is 128 consecutive rows; the V warps
-//               look for rows of zeros first
+//               look for rows of zeros and unusual scales first
 //   warps 20-21 resolve positions to cache rows, scales and masks, a block
 //               each in turn, ahead of the copies (a ring of three blocks)
 //   warps 22-23 rank 0: issue the MMAs, 22 Q K^T as soon as a block's K is there
@@ -125,7 +125,7 @@ constexpr float TOP = 4.f, SLACK = 4.5f;       // log2 of the largest weight whe
 
 struct __align__(8) Bars {
     uint64_t info_full[RING];        // positions, scales and masks of a block are there
-    uint64_t scale_full[RING];       // and its rows of zeros are known (both V warps)
+    uint64_t scale_full[RING];       // and weigh_scales is through (both V warps)
     uint64_t info_free[2 * RING];    // block j % 6 has been used: always waited for by the same warp
     uint64_t q_full;                 // rank 0: Q of a unit is in place (both CTAs' warps)
     uint64_t k_full[2], v_full[2];   // own tiles have landed
@@ -345,6 +345,11 @@ __device__ __forceinline__ uint32_t random_start(uint32_t row, uint32_t at) {
     return x ^ x >> 15;
 }
 __device__ __forceinline__ uint32_t random_next(uint32_t x) { return x * 1664525u + 1013904223u; }
+__device__ __forceinline__ float reciprocal(float a) {       // within 2^-23 of itself, subnormal results too
+    float d;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(d) : "f"(a));
+    return d;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -391,39 +396,46 @@ __device__ __forceinline__ int part_col(int warp, int c) {
     return 256 * (warp >> 3) + 128 * ((warp >> 1) & 1) + 64 * ((warp >> 2) & 1) + 32 * c;
 }
 
+// What the resolution leaves of the scales of a block, for 64 of its keys (one
+// warp, while it waits for its stage):
+//
 // A row whose codes are all 0 adds nothing to O, whatever its weight there.  The
 // writer gives it the scale 1, far above that of small values: p_s * 1 as its
 // weight would set the row's maximum and put the others under the range of 8
 // bits.  It gets the weight 2^-NIL p_s instead, below p_s times any scale that the
-// writer gives, and the same part in the softmax sum as ever.  One warp, 64 keys:
-// those of scale 1 whose first 16 codes are 0 are read whole, 16 bytes a lane.
+// writer gives, and the same part in the softmax sum as ever.  Keys of scale 1
+// whose first 16 codes are 0 are read whole, 16 bytes a lane.
+// A scale that is no power of two (another rule's) gets its logarithm and inverse.
+//
 // 128 lists, one row in a thousand zero: 85.0 -> 87.2 us.  (In the warps that
 // resolve positions, a load behind the scales: 90; in the softmax warps: 98; in a
 // warp of its own, with 72 registers a thread for all: 96; for rows of any scale:
 // 97.)
 constexpr int NIL = 40;
 __device__ __forceinline__ bool no_codes(uint4 v) { return ((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) == 0; }
-__device__ __forceinline__ void weigh_rows_of_zeros(Info& info, const uint8_t* cache, int key0, int lane) {
-    uint32_t nil[2];                        // keys key0 + lane and 32 after it
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int key = key0 + 32 * i + lane, row = info.rows[key];
-        bool maybe = info.scale[key] == 1.f && row >= 0;
-        if (maybe) maybe = no_codes(__ldg(reinterpret_cast<const uint4*>(cache + (int64_t)row * ROW)));   // the first 16
-        nil[i] = __ballot_sync(0xffffffffu, maybe);
-    }
-    if (!(nil[0] | nil[1])) return;
+__device__ __forceinline__ void weigh_scales(Info& info, const uint8_t* cache, int key0, int lane) {
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-        const int* rows = info.rows + key0 + 32 * i;
+    for (int i = 0; i < 64; i += 32) {
+        const int key = key0 + i + lane, row = info.rows[key];
+        const float g = info.scale[key];
+        const uint32_t u = __float_as_uint(g);
+        // a power of two that has an inverse, and not 1: ready
+        if (!__any_sync(0xffffffffu, (u & 0x807fffffu) != 0 || u - 0x00800000u >= 0x7e800000u || u == 0x3f800000u)) continue;
+        if (((u & 0x7fffffu) != 0 || u >= 0x7f000000u) && u - 0x00800000u < 0x7f000000u) {
+            info.lg[key] = (float)((int)(u >> 23) - 127) + __log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u));
+            info.inv[key] = reciprocal(g);
+        }
+        bool nil = u == 0x3f800000u && row >= 0;
+        if (nil) nil = no_codes(__ldg(reinterpret_cast<const uint4*>(cache + (int64_t)row * ROW)));        // the first 16
 #pragma unroll 1
-        for (uint32_t left = i ? nil[1] : nil[0]; left;) {
-            const int l = __ffs(left) - 1;
-            left &= left - 1;
-            if (__all_sync(0xffffffffu, no_codes(__ldg(reinterpret_cast<const uint4*>(cache + (int64_t)rows[l] * ROW) + lane))) && lane == 0) {
-                info.lg[key0 + 32 * i + l] = -(float)NIL;
-                info.inv[key0 + 32 * i + l] = exp2_int(NIL);
-            }
+        for (uint32_t left = __ballot_sync(0xffffffffu, nil); left; left &= left - 1) {
+            const int64_t r = info.rows[key0 + i + __ffs(left) - 1];
+            const bool all = __all_sync(0xffffffffu, no_codes(__ldg(reinterpret_cast<const uint4*>(cache + r * ROW) + lane)));
+            if (lane == __ffs(left) - 1) nil = all;
+        }
+        if (nil) {
+            info.lg[key] = -(float)NIL;
+            info.inv[key] = exp2_int(NIL);
         }
     }
 }
@@ -908,7 +920,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
             const uint32_t buf = j & 1;
             ok = wait_for(&s.info_full[slot], turn & 1, status, abort, 1);
             if (ok && !is_k) {
-                weigh_rows_of_zeros(reinterpret_cast<Info*>(smem + OFF_INFO)[slot], a.cache, mine * 64, lane);
+                weigh_scales(reinterpret_cast<Info*>(smem + OFF_INFO)[slot], a.cache, mine * 64, lane);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.scale_full[slot]);
             }
@@ -1004,9 +1016,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap map_box,     // box: 64 row
                 word |= __shfl_xor_sync(0xffffffffu, word, 4);
                 float lg[4], inv[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {          // a power of two
-                    const uint32_t u = __float_as_uint(g[i]) & 0x7f800000u;
-                    g[i] = __uint_as_float(u);
+                for (int i = 0; i < 4; ++i) {          // of a power of two (others: weigh_scales)
+                    const uint32_t u = __float_as_uint(g[i]);
                     lg[i] = (float)((int)(u >> 23) - 127);
                     inv[i] = __uint_as_float(0x7f000000u - u);
                 }

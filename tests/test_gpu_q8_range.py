@@ -1,6 +1,7 @@
 """The attention over the quantised cache where softmax weights span a wide
-range: long contexts under one large weight, rows of zeros.  Compared with the
-definition in 64 bits; caches come from ic_cache_write_q8.
+range: long contexts under one large weight, rows of zeros, scales of any
+kind.  Compared with the definition in 64 bits; caches come from
+ic_cache_write_q8 unless a test makes its own.
 
 Tolerance, elementwise, with softmax weights p_s (normalised), scales g_s,
 codes c_s, V_s = g_s c_s and w_s = p_s g_s.  Nothing in it is a bias that adds
@@ -230,3 +231,39 @@ def test_many_rows_of_zeros():
     check(attend(q, cache, scale, [n])[0, 0], ref, tol, "pages of zeros")
     cache, scale = packed(torch.zeros(300, 576, device=D))
     assert (attend(q, cache, scale, [300]) == 0).all()
+
+
+# ---------------------------------------------------------------- scales
+@pytest.mark.parametrize("listed", [False, True])
+def test_scales_that_are_no_powers_of_two(listed):
+    """A cache that was filled by another rule: absmax / 448."""
+    n = 900
+    g = torch.Generator(device=D).manual_seed(7)
+    kv = torch.randn(n, 576, device=D, generator=g) * torch.exp(torch.randn(n, 1, device=D, generator=g))
+    scale = torch.ones(1024, device=D)
+    scale[:n] = kv[:, :512].abs().amax(1) / 448.0
+    cache = torch.zeros(1024, 640, dtype=torch.uint8, device=D)
+    cache[:n, :512] = (kv[:, :512] / scale[:n, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    cache[:n, 512:] = (kv[:, 512:] / scale[:n, None]).to(BF).view(torch.uint8).view(n, 128)
+    q = torch.randn(1, 2, 70, 576, device=D, generator=g).to(BF)
+    idx = None
+    if listed:
+        idx = torch.stack([torch.randperm(n - 2, device=D, generator=g)[:333] for _ in range(2)]).view(1, 2, 333).to(torch.int32)
+    out = attend(q, cache, scale, [n], idx=idx)
+    for i in range(2):
+        at = torch.arange(n - 1 + i, device=D) if idx is None else idx[0, i].long()
+        ref, tol = exact(q[0, i], cache, scale, at, 576 ** -0.5)
+        check(out[0, i], ref, tol, "node %d" % i)
+
+
+def test_large_and_small_scales():
+    """One value in each row far from the others' sizes: scales 2^-32 to 2^40 in turn, one at a time."""
+    g = torch.Generator(device=D).manual_seed(8)
+    q = torch.randn(1, 1, 8, 576, device=D, generator=g).to(BF)
+    for e in (-32, -20, 0, 25, 40):
+        kv = torch.randn(200, 576, device=D, generator=g) * 2.0 ** e * 100
+        kv[:, :512].clamp_(-300 * 2.0 ** e, 300 * 2.0 ** e)
+        cache, scale = packed(kv)
+        factor = 2.0 ** -e / 2400
+        ref, tol = exact(q[0, 0], cache, scale, torch.arange(200, device=D), factor)
+        check(attend(q, cache, scale, [200], factor=factor)[0, 0], ref, tol, "scale 2^%d" % e)

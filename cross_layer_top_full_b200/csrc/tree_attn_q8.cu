@@ -405,7 +405,10 @@ __device__ __forceinline__ int part_col(int warp, int c) {
 // bits.  It gets the weight 2^-NIL p_s instead, below p_s times any scale that the
 // writer gives, and the same part in the softmax sum as ever.  Keys of scale 1
 // whose first 16 codes are 0 are read whole, 16 bytes a lane.
+// A row of zeros with the scale 0 does as well (one that nothing was written to).
 // A scale that is no power of two (another rule's) gets its logarithm and inverse.
+// One that is no positive normal number makes the logits, and so the rows that
+// see the key, NaN; its inverse stays finite, for the sums of the rows that do not.
 //
 // 128 lists, one row in a thousand zero: 85.0 -> 87.2 us.  (In the warps that
 // resolve positions, a load behind the scales: 90; in the softmax warps: 98; in a
@@ -421,11 +424,12 @@ __device__ __forceinline__ void weigh_scales(Info& info, const uint8_t* cache, i
         const uint32_t u = __float_as_uint(g);
         // a power of two that has an inverse, and not 1: ready
         if (!__any_sync(0xffffffffu, (u & 0x807fffffu) != 0 || u - 0x00800000u >= 0x7e800000u || u == 0x3f800000u)) continue;
-        if (((u & 0x7fffffu) != 0 || u >= 0x7f000000u) && u - 0x00800000u < 0x7f000000u) {
+        const bool normal = u - 0x00800000u < 0x7f000000u;
+        if (normal && ((u & 0x7fffffu) != 0 || u >= 0x7f000000u)) {
             info.lg[key] = (float)((int)(u >> 23) - 127) + __log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u));
             info.inv[key] = reciprocal(g);
         }
-        bool nil = u == 0x3f800000u && row >= 0;
+        bool nil = (u == 0x3f800000u || g == 0.f) && row >= 0;
         if (nil) nil = no_codes(__ldg(reinterpret_cast<const uint4*>(cache + (int64_t)row * ROW)));        // the first 16
 #pragma unroll 1
         for (uint32_t left = __ballot_sync(0xffffffffu, nil); left; left &= left - 1) {
@@ -436,6 +440,9 @@ __device__ __forceinline__ void weigh_scales(Info& info, const uint8_t* cache, i
         if (nil) {
             info.lg[key] = -(float)NIL;
             info.inv[key] = exp2_int(NIL);
+        } else if (!normal) {
+            info.scale[key] = __uint_as_float(0x7fffffffu);
+            info.inv[key] = 1.f;
         }
     }
 }

@@ -516,7 +516,9 @@ ic_status ic_cache_read_q8(const void* kv_q8, const float* kv_scale, const void*
  * same call gives the same bits.  The scales of the positions that a row sees should
  * lie within 2^90 of one another (float32's range).
  * A NaN or infinity in a cache row that a query row does not see does not
- * reach that row's output; a NaN in a seen row makes it NaN.
+ * reach that row's output, and neither does its scale; a NaN in a seen row makes
+ * it NaN, and so does a scale that is no positive normal number (but 0 above codes
+ * that are all 0: a row of zeros).
  * Batches of 2^28 blocks or more (blocks of 128 positions of T_max or of k, for
  * each row of a list or each 128 (node, head) pairs) return IC_ERR_UNSUPPORTED.
  * Workspace: ic_tree_attn_q8_workspace_size(pr, k, Hq). */

@@ -267,3 +267,44 @@ def test_large_and_small_scales():
         factor = 2.0 ** -e / 2400
         ref, tol = exact(q[0, 0], cache, scale, torch.arange(200, device=D), factor)
         check(attend(q, cache, scale, [200], factor=factor)[0, 0], ref, tol, "scale 2^%d" % e)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf"), -0.5, 0.0, 1e-40])
+@pytest.mark.parametrize("listed", [False, True])
+def test_a_bad_scale_stays_where_it_is_seen(bad, listed):
+    """A scale that is no positive normal number makes the rows that see it NaN, and no others."""
+    n, Lq, Hq = 200, 5, 20
+    g = torch.Generator(device=D).manual_seed(9)
+    cache, scale = packed(torch.randn(n, 576, device=D, generator=g))
+    scale[196] = bad                                                     # node 1
+    q = torch.randn(1, Lq, Hq, 576, device=D, generator=g).to(BF)
+    masks = [1, 3, 1 | 4, 1 | 8, 1 | 2 | 16]
+    tree = torch.tensor([masks], dtype=torch.int64, device=D)
+    idx = torch.arange(n, dtype=torch.int32, device=D).expand(1, Lq, n).contiguous() if listed else None
+    out = attend(q, cache, scale, [n], idx=idx, tree=tree)
+    for i, mask in enumerate(masks):
+        if mask & 2:
+            assert torch.isnan(out[0, i]).all(), i
+            continue
+        at = torch.tensor([s for s in range(n) if s < 195 or mask >> (s - 195) & 1], device=D)
+        ref, tol = exact(q[0, i], cache, scale, at, 576 ** -0.5, group=at)
+        check(out[0, i], ref, tol, "node %d" % i)
+
+
+@pytest.mark.parametrize("listed", [False, True])
+def test_rows_that_were_never_written_are_rows_of_zeros(listed):
+    """Bytes and scales of a fresh cache, all 0, among small values."""
+    n = 300
+    g = torch.Generator(device=D).manual_seed(10)
+    cache, scale = packed(torch.randn(n, 576, device=D, generator=g) * 1e-3)
+    fresh = torch.tensor([17, 250], device=D)
+    cache[fresh], scale[fresh] = 0, 0.0
+    ones = scale.clone()
+    ones[fresh] = 1.0
+    q = torch.randn(1, 3, 11, 576, device=D, generator=g).to(BF)
+    idx = torch.arange(n, dtype=torch.int32, device=D).expand(1, 3, n).contiguous() if listed else None
+    out = attend(q, cache, scale, [n], idx=idx)
+    for i in range(3):
+        ref, tol = exact(q[0, i], cache, ones, torch.arange(n - 2 + i, device=D), 576 ** -0.5)
+        check(out[0, i], ref, tol, "node %d" % i)
+    assert (attend(q, cache * 0, scale * 0, [n], idx=idx) == 0).all()

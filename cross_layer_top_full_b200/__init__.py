@@ -14,6 +14,7 @@ their ``*_workspace_size`` queries, ``workspace_init``, ``read_status``,
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Dict, List, Optional, Sequence
 
@@ -459,12 +460,15 @@ class _Torch:
         # without it, or where it declines, the calls below make them here.
         self.tensor, self.fast = torch.Tensor, None
         try:
-            from . import _fastcall
-        except ImportError:
+            from .build import fast_path                 # of this torch and this Python only
+            spec = importlib.util.spec_from_file_location(__name__ + "._fastcall", fast_path())
+            fast = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(fast)
+        except (ImportError, OSError):
             return
-        _fastcall.bind(*(ctypes.cast(f, _P).value for f in (
+        fast.bind(*(ctypes.cast(f, _P).value for f in (
             lib().ic_cache_write_q8, lib().ic_cache_read_q8, lib().ic_tree_attn_q8_paged)))
-        self.fast = _fastcall
+        self.fast = fast
 
 
 _torch: Optional[_Torch] = None

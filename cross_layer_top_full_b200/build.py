@@ -4,13 +4,15 @@
 ``csrc/*.cu`` with nvcc for ``sm_100a`` and links ``libindexcache.so`` next to
 this file.  Objects go to ``_build/`` and are rebuilt only when a source or
 header is newer.  Where torch is installed, ``csrc/fastcall.cpp`` becomes
-``_fastcall.so``: the short way of the quantised-cache calls from Python.
+``_fastcall.<tag>.so``: the short way of the quantised-cache calls from Python.
+It reads tensors through torch's own inline code, so the tag names the torch and
+the Python that it was compiled for, and no others load it.  The calls work
+without it, and so does the build.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
-import importlib.util
 import os
 import shutil
 import subprocess
@@ -23,7 +25,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libindexcache.so")
-FAST = os.path.join(PKG, "_fastcall.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -60,23 +61,46 @@ def _compile(nvcc: str, src: str, verbose: bool, ptxas_v: bool) -> str:
     return obj
 
 
+def fast_path() -> str:
+    """Path of the short way's module for the torch and the Python that run."""
+    import torch
+    return os.path.join(PKG, "_fastcall.%s.torch-%s-%s.abi%d.so" % (
+        sysconfig.get_config_var("SOABI"), torch.__version__, (torch.version.git_version or "")[:8],
+        torch._C._GLIBCXX_USE_CXX11_ABI))
+
+
 def _build_fastcall(verbose: bool) -> None:
-    spec = importlib.util.find_spec("torch")
-    if spec is None:
+    try:
+        import torch
+    except ImportError:
         return
+    fast = fast_path()
+    for old in glob.glob(os.path.join(os.path.dirname(fast), "_fastcall*.so")):
+        if old != fast:
+            os.remove(old)
     src, header = os.path.join(CSRC, "fastcall.cpp"), os.path.join(INCLUDE, "indexcache.h")
-    if os.path.exists(FAST) and os.path.getmtime(FAST) >= max(os.path.getmtime(src), os.path.getmtime(header)):
+    if os.path.exists(fast) and os.path.getmtime(fast) >= max(os.path.getmtime(src), os.path.getmtime(header)):
         return
-    torch = os.path.dirname(spec.origin)
-    libs = os.path.join(torch, "lib")
+    root = os.path.dirname(torch.__file__)
+    libs = os.path.join(root, "lib")
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-           "-I", INCLUDE, "-I", os.path.join(torch, "include"),
-           "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
-           "-I", sysconfig.get_paths()["include"], src, "-o", FAST,
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-I", INCLUDE, "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], src, "-o", fast,
            "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + libs]
     if verbose:
         print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        error = res.stderr if res.returncode else None
+    except OSError as e:                                 # no compiler
+        error = "%s\n" % e
+    if error is not None:
+        if os.path.exists(fast):                         # of older sources
+            os.remove(fast)
+        sys.stderr.write(error + "csrc/fastcall.cpp did not compile: the quantised-cache calls from Python go "
+                                 "the long way\n")
 
 
 def build(verbose: bool = False, ptxas_v: bool = False) -> str:

@@ -24,8 +24,8 @@
 //     of themselves down to 2^-6, then a step of 2^-13, of a quarter of the
 //     weight under 2^-11, of 2^-16 at last.  That costs 1.5 %, the largest weight
 //     at 2^4 instead of 2^2 (two more bits for the others, more maxima that
-//     outgrow their room) another 2 %: 128 lists of 2048, 82.7, 84.1, 85.9 us;
-//     with 2^6 89.3.  The softmax sum adds w_s / g_s in float32, before that
+//     outgrow their room) another 2 %: 128 lists of 2048 over the same inputs,
+//     82.7, 84.1, 85.9 us; with 2^6 89.3.  The softmax sum adds w_s / g_s in float32, before that
 //     rounding.
 // Two 8-bit products cost what one of bfloat16 does, without the decoding and
 // with 644 bytes of cache traffic per row.
@@ -41,8 +41,10 @@
 // hold to 60 % of their rate; P V 1,060 at the full rate); blocks in a row
 // take 2,800 to 2,900, the two products overlapping.  A unit costs 18,000
 // cycles besides, for Q, the first block's latency and the results.
-// 128 lists of 2048 (73 GFLOP): 97 us; 8 sequences of up to 8192 with 16 nodes,
-// every position (159 GFLOP): 168 us; 32 lists: 37 us; one list: 17 us.
+// 128 lists of 2048 (73 GFLOP): 102 us; 8 sequences of up to 8192 with 16 nodes,
+// every position (159 GFLOP): 173 us; 32 lists: 38.5 us; one list: 17.5 us (a
+// pass among others, other inputs each; over the same inputs again, as the steps
+// below were compared, 88, 150 to 160, 36.3 and 17.7).
 // Steps that did not help: four-row TMA gathers (about 65 cycles each, 112 a
 // block, against 36 cp.async a warp), a wait of the copies' arrival by the MMA
 // warp with its proxy fence there, releases at cluster scope for the arrivals
@@ -404,7 +406,7 @@ __device__ __forceinline__ int part_col(int warp, int c) {
 // weight would set the row's maximum and put the others under the range of 8
 // bits.  It gets the weight 2^-NIL p_s instead, below p_s times any scale that the
 // writer gives, and the same part in the softmax sum as ever.  Keys of scale 1
-// whose first 16 codes are 0 are read whole, 16 bytes a lane.
+// whose first 16 codes are 0 are read whole, up to four at once, eight lanes each.
 // A row of zeros with the scale 0 does as well (one that nothing was written to).
 // A scale that is no power of two (another rule's) gets its logarithm and inverse.
 // One that is no positive normal number makes the logits, and so the rows that
@@ -413,7 +415,8 @@ __device__ __forceinline__ int part_col(int warp, int c) {
 // 128 lists, one row in a thousand zero: 85.0 -> 87.2 us.  (In the warps that
 // resolve positions, a load behind the scales: 90; in the softmax warps: 98; in a
 // warp of its own, with 72 registers a thread for all: 96; for rows of any scale:
-// 97.)
+// 97.)  A cache of zeros alone takes three times as long (261 us; one row at a
+// time 579).
 constexpr int NIL = 40;
 __device__ __forceinline__ bool no_codes(uint4 v) { return ((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) == 0; }
 __device__ __forceinline__ void weigh_scales(Info& info, const uint8_t* cache, int key0, int lane) {
@@ -431,11 +434,19 @@ __device__ __forceinline__ void weigh_scales(Info& info, const uint8_t* cache, i
         }
         bool nil = (u == 0x3f800000u || g == 0.f) && row >= 0;
         if (nil) nil = no_codes(__ldg(reinterpret_cast<const uint4*>(cache + (int64_t)row * ROW)));        // the first 16
+        const uint32_t asked = __ballot_sync(0xffffffffu, nil);
 #pragma unroll 1
-        for (uint32_t left = __ballot_sync(0xffffffffu, nil); left; left &= left - 1) {
-            const int64_t r = info.rows[key0 + i + __ffs(left) - 1];
-            const bool all = __all_sync(0xffffffffu, no_codes(__ldg(reinterpret_cast<const uint4*>(cache + r * ROW) + lane)));
-            if (lane == __ffs(left) - 1) nil = all;
+        for (int k = 0; k < 32; k += 4) {                   // 4 rows at once
+            if (!((asked >> k) & 0xfu)) continue;
+            const int mine = k + lane / 8;
+            bool all = true;
+            if ((asked >> mine) & 1u) {
+                const uint4* p = reinterpret_cast<const uint4*>(cache + (int64_t)info.rows[key0 + i + mine] * ROW) + lane % 8;
+#pragma unroll 4
+                for (int c = 0; c < 32; c += 8) all = no_codes(__ldg(p + c)) && all;
+            }
+            const uint32_t yes = __ballot_sync(0xffffffffu, all);
+            if (lane >= k && lane < k + 4 && ((yes >> ((lane - k) * 8)) & 0xffu) != 0xffu) nil = false;
         }
         if (nil) {
             info.lg[key] = -(float)NIL;
@@ -474,8 +485,9 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int row0, const uint8_t*
 // The 64 rows of this CTA, 512 threads: a warp takes 4 rows, a lane 16 of the
 // coded columns and 8 of the others.  What goes to tensor memory (lane = row)
 // passes through the P tiles, which are free once P V of block j - 1 is
-// complete.  A row with an infinity or a NaN becomes NaN as a whole (its
-// outputs are).  Returns the scale of this thread's row.
+// complete.  A row with an infinity or a NaN in its coded columns becomes NaN as
+// a whole (its outputs are); in the others it goes into the logits as it is.
+// Returns the scale of this thread's row.
 __device__ __forceinline__ float convert_q(const Args& a, const Rows& r, uint8_t* smem, Bars& s, uint32_t rank,
                                            uint32_t tmem, uint32_t lane_base, uint32_t j, uint32_t q_bar) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1323,9 +1335,12 @@ ic_status launch_tree_attn_q8(const void* q, const void* kv_q8, const float* kv_
     count_launch(IC_LK_TREE);
     ic_status st = last_launch_status();
     if (st != IC_OK || p.sharing == WHOLE || p.list_blocks == 1) return st;     // no partial results
-    // few runs: one piece a warp and every run at once, for the latency of many
-    // runs of one unit; else more pieces a warp, the fewer runs a unit has
-    // (8 a unit: 9.4 us with four pieces, 5.7 with two; 2 a unit: 5.3 and 7.0)
+    // Up to 32 pairs: one piece a warp and 16 runs at once, for the latency of
+    // many runs of one unit.  More pairs: as for many units, more pieces a warp
+    // the fewer runs a unit has (8 a unit: 9.4 us with four pieces, 5.7 with two;
+    // 2 a unit: 5.3 and 7.0).  One long unit over all 74 pairs falls under the
+    // second rule, where 256 warps read its runs four at a time: 60,000 positions
+    // of one sequence take 57 us in all, and its bytes and operations 10.4.
     const bool few = p.pairs <= 32;
     const int64_t units = (int64_t)pr.B * p.units;
     auto join = few ? tree_join_kernel<1, 16, 1> : p.pairs / units > 2 ? tree_join_kernel<2, 4, 2> : tree_join_kernel<4, 2, 2>;

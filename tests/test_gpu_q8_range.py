@@ -233,6 +233,23 @@ def test_many_rows_of_zeros():
     assert (attend(q, cache, scale, [300]) == 0).all()
 
 
+def test_a_single_value_is_no_row_of_zeros():
+    """Rows of scale 1 with one value anywhere, rows of zeros beside them."""
+    n = 700
+    g = torch.Generator(device=D).manual_seed(11)
+    kv = torch.zeros(n, 576, device=D)
+    kv[::5] = torch.randn(140, 576, device=D, generator=g)
+    columns = torch.arange(512, device=D)
+    at = torch.arange(n, device=D)[torch.arange(n, device=D) % 5 != 0][:512]
+    kv[at, columns] = 300.0 * (1 - 2 * (columns % 2))
+    q = torch.zeros(1, 1, 9, 576, device=D)
+    q[..., 512:] = torch.randn(1, 1, 9, 64, device=D, generator=g)
+    q = q.to(BF)
+    cache, scale = packed(kv)
+    ref, tol = exact(q[0, 0], cache, scale, torch.arange(n, device=D), 576 ** -0.5)
+    check(attend(q, cache, scale, [n])[0, 0], ref, tol, "one value a row")
+
+
 # ---------------------------------------------------------------- scales
 @pytest.mark.parametrize("listed", [False, True])
 def test_scales_that_are_no_powers_of_two(listed):

@@ -490,8 +490,8 @@ ic_status ic_cache_read_q8(const void* kv_q8, const float* kv_scale, const void*
  *
  *   q         [B, Lq, Hq, 576] bf16, Hq in [1, 128], 16-byte aligned
  *   kv_q8     [num_pages*page_size, IC_Q8_ROW_BYTES], 16-byte aligned
- *   kv_scale  [num_pages*page_size] float32, positive normal numbers (the write
- *             gives powers of two; other rules' caches read as they are)
+ *   kv_scale  [num_pages*page_size] float32, positive numbers of 2^-96 or more
+ *             (the write gives powers of two; other rules' caches read as they are)
  *   idx       [B, Lq, k] int32 logical positions, or -1 (skipped, anywhere in
  *             the row).  A node that the row does not see is skipped too.  A
  *             position outside [0, seq_lens[b]) and not -1 is skipped and
